@@ -213,6 +213,113 @@ SGEMM_API int gemm_f16_f32(int M, int N, int K,
                  void *stream);
 
 /*
+ * Microscaled 4-bit floating point (MXFP4): the element and block formats of
+ * the OCP Microscaling Formats (MX) specification 1.0, E2M1 elements in blocks
+ * of 32 with an E8M0 scale, multiplied on the matrix cores
+ * (v_mfma_scale_f32_16x16x128_f8f6f4).
+ *
+ * An MXFP4 matrix of R rows and K columns is two byte matrices:
+ * - values Q: row r's ceil(K/2) bytes at Q + r*ldq.  Byte i holds element 2i
+ *   in its low and 2i+1 in its high half; where K is odd, the last byte's high
+ *   half belongs to no element (written as 0, never looked at).  An element is
+ *   sign, two exponent bits, one mantissa bit: codes 0..7 are 0, 0.5, 1, 1.5,
+ *   2, 3, 4, 6, codes 8..15 their negatives;
+ * - scales S: row r's ceil(K/32) bytes at S + r*lds.  Byte j scales elements
+ *   32j .. 32j+31 by 2^(byte - 127); byte 255 makes them all NaN.
+ * Leading dimensions of both count bytes.  Pointers and leading dimensions may
+ * have any alignment; rows of Q that are 16-byte aligned (base and ld) take
+ * the fast loaders.
+ *
+ * Common to these entry points: device pointers, stream order, validation
+ * before any HIP call and the return codes are as above (SGEMM_EINVAL_LD also
+ * for a leading dimension below a row's bytes, SGEMM_EALIAS also for an output
+ * that overlaps an input or another output; extents run from a matrix's first
+ * byte to its last row's end, so scales may not lie between the rows of the
+ * values they belong to).  Bytes outside the R rows and their row lengths are
+ * neither read nor written.  Nothing is allocated, no workspace is used, and
+ * every result is the same from call to call.
+ */
+
+/*
+ * Quantise X (R x C, row-major, ldx in elements) to MXFP4, in one pass over X:
+ * - along its rows into (Q, S): an R x C MXFP4 matrix;
+ * - along its columns into (QT, ST): the C x R MXFP4 matrix of X transposed,
+ *   its blocks running down X's columns.
+ * Either pair may be NULL, then its leading dimensions are not looked at;
+ * both NULL or half a pair -> SGEMM_EINVAL_PTR.  With both, X is read once.
+ * For a block of values with the largest magnitude t the scale's exponent is
+ * floor(log2 t) - 2, at least -127 (t == 0: -127); each value x becomes the
+ * element nearest to x / scale, ties to the even code, magnitudes beyond 6 to
+ * 6.  Signs are kept, also of zeros.  A block that holds a NaN or an infinity
+ * gets scale byte 255, its codes are unspecified.  The last block of a row
+ * takes its largest magnitude from the elements that exist.
+ * _f32 takes float, _bf16 and _f16 raw 16-bit storage.
+ */
+SGEMM_API int gemm_mxfp4_quantize_f32(int R, int C, const void *X, int ldx,
+                            void *Q, int ldq, void *S, int lds,
+                            void *QT, int ldqt, void *ST, int ldst,
+                            void *stream);
+SGEMM_API int gemm_mxfp4_quantize_bf16(int R, int C, const void *X, int ldx,
+                             void *Q, int ldq, void *S, int lds,
+                             void *QT, int ldqt, void *ST, int ldst,
+                             void *stream);
+SGEMM_API int gemm_mxfp4_quantize_f16(int R, int C, const void *X, int ldx,
+                            void *Q, int ldq, void *S, int lds,
+                            void *QT, int ldqt, void *ST, int ldst,
+                            void *stream);
+
+/*
+ * Y (R x C, row-major, ldy in elements) = the values of an MXFP4 matrix.
+ * float and bfloat16 hold every finite one exactly, but for magnitudes of
+ * 2^128 and more (scale bytes 253 and above), which become infinite; _f16
+ * rounds to nearest even, to infinity beyond its range.
+ */
+SGEMM_API int gemm_mxfp4_dequantize_f32(int R, int C, const void *Q, int ldq,
+                              const void *S, int lds, void *Y, int ldy, void *stream);
+SGEMM_API int gemm_mxfp4_dequantize_bf16(int R, int C, const void *Q, int ldq,
+                               const void *S, int lds, void *Y, int ldy, void *stream);
+SGEMM_API int gemm_mxfp4_dequantize_f16(int R, int C, const void *Q, int ldq,
+                              const void *S, int lds, void *Y, int ldy, void *stream);
+
+/*
+ * C = A.B^T with A (M x K) and B (N x K) in MXFP4, both blocked along K:
+ *     C[i,j] = sum_k A[i,k] * B[j,k]
+ * accumulated in fp32 (products with their scales are exact there), C fp32 or
+ * bfloat16 (rounded once, to nearest even).  B's rows are the product's
+ * columns: a layer's weights, outputs x inputs, are used as they are stored.
+ * The three products of a linear layer Y = X.W^T are
+ *     Y  = A.B^T of X and W, each quantised along its rows,
+ *     dX = A.B^T of dY (rows) and W (columns: its QT, ST),
+ *     dW = A.B^T of dY and X, both quantised along their columns.
+ * K == 0 stores zeros.  M of at most 64 streams B once.
+ */
+SGEMM_API int gemm_mxfp4_f32(int M, int N, int K,
+                   const void *A, int lda, const void *SA, int ldsa,
+                   const void *B, int ldb, const void *SB, int ldsb,
+                   float *C, int ldc, void *stream);
+SGEMM_API int gemm_mxfp4_bf16(int M, int N, int K,
+                    const void *A, int lda, const void *SA, int ldsa,
+                    const void *B, int ldb, const void *SB, int ldsb,
+                    void *C, int ldc, void *stream);
+
+/*
+ * C = A.B^T with 16-bit A (M x K, row-major, lda in elements) and B (N x K) in
+ * MXFP4 blocked along K, fp32 accumulate and C: weights kept in four bits,
+ * activations as they are.  Products are exact in fp32, so the result is
+ * within the fp32 rounding of some summation order of the exact products.  An
+ * element of B of magnitude 2^128 or more (possible at scale bytes 253 and
+ * above) makes the outputs it contributes to infinite or NaN.  K == 0 stores zeros.  M of at most 64 streams B once.
+ */
+SGEMM_API int gemm_bf16_mxfp4_f32(int M, int N, int K,
+                        const void *A, int lda,
+                        const void *B, int ldb, const void *SB, int ldsb,
+                        float *C, int ldc, void *stream);
+SGEMM_API int gemm_f16_mxfp4_f32(int M, int N, int K,
+                       const void *A, int lda,
+                       const void *B, int ldb, const void *SB, int ldsb,
+                       float *C, int ldc, void *stream);
+
+/*
  * The micro-GEMM of "Micro Kernel 입문하기" (teach-meaning.tistory.com/1544),
  * section 2: one GPU thread holds the whole 4x4 tile of C in 16 registers and
  * walks k = 0..K-1 in order, loading column k of A (4 values) and row k of B

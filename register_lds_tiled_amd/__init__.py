@@ -10,4 +10,7 @@ from .binding import (  # noqa: F401
     PATH_AUTO, PATH_MFMA, PATH_VALU, PATH_VALU_PAGE, PATHS, SgemmError, matmul,
     sgemm_abi_version, sgemm_f32, sgemm_f32_path, sgemm_last_error,
     sgemm_micro4x4_f32, sgemm_status_string,
+    gemm_bf16_mxfp4_f32, gemm_f16_mxfp4_f32, gemm_mxfp4_bf16, gemm_mxfp4_dequantize_bf16,
+    gemm_mxfp4_dequantize_f16, gemm_mxfp4_dequantize_f32, gemm_mxfp4_f32,
+    gemm_mxfp4_quantize_bf16, gemm_mxfp4_quantize_f16, gemm_mxfp4_quantize_f32,
 )

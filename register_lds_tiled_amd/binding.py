@@ -40,7 +40,10 @@ PATHS = {"auto": PATH_AUTO, "valu": PATH_VALU, "mfma": PATH_MFMA, "valu_page": P
 EXPORTS = ("sgemm_f32", "sgemm_f32_path", "sgemm_f32_ex", "gemm_bf16_f32", "gemm_f16_f32",
            "sgemm_micro4x4_f32", "sgemm_f32_valu_tile", "sgemm_valu_tile_count",
            "sgemm_valu_tile_name", "sgemm_status_string", "sgemm_last_error",
-           "sgemm_abi_version")
+           "sgemm_abi_version", "gemm_mxfp4_quantize_f32", "gemm_mxfp4_quantize_bf16",
+           "gemm_mxfp4_quantize_f16", "gemm_mxfp4_dequantize_f32", "gemm_mxfp4_dequantize_bf16",
+           "gemm_mxfp4_dequantize_f16", "gemm_mxfp4_f32", "gemm_mxfp4_bf16",
+           "gemm_bf16_mxfp4_f32", "gemm_f16_mxfp4_f32")
 
 _lib = None
 _lib_poison = None
@@ -83,6 +86,15 @@ def _load(path: str):
     lib.sgemm_valu_tile_count.restype = i
     lib.sgemm_valu_tile_name.argtypes = [i]
     lib.sgemm_valu_tile_name.restype = ctypes.c_char_p
+    for t in ("f32", "bf16", "f16"):
+        fn = getattr(lib, f"gemm_mxfp4_quantize_{t}")
+        fn.argtypes, fn.restype = [i, i, p, i, p, i, p, i, p, i, p, i, p], i
+        fn = getattr(lib, f"gemm_mxfp4_dequantize_{t}")
+        fn.argtypes, fn.restype = [i, i, p, i, p, i, p, i, p], i
+    for fn in (lib.gemm_mxfp4_f32, lib.gemm_mxfp4_bf16):
+        fn.argtypes, fn.restype = [i, i, i, p, i, p, i, p, i, p, i, p, i, p], i
+    for fn in (lib.gemm_bf16_mxfp4_f32, lib.gemm_f16_mxfp4_f32):
+        fn.argtypes, fn.restype = [i, i, i, p, i, p, i, p, i, p, i, p], i
     lib.sgemm_status_string.argtypes = [i]
     lib.sgemm_status_string.restype = ctypes.c_char_p
     lib.sgemm_last_error.argtypes = []
@@ -241,6 +253,131 @@ def sgemm_valu_tile_name(tile: int):
 def valu_tiles():
     """{index: description} of the VALU path's built tile configurations."""
     return {t: sgemm_valu_tile_name(t) for t in range(sgemm_valu_tile_count())}
+
+
+# ---- MXFP4: 4-bit elements in blocks of 32 with one scale byte each --------
+
+_MX_KINDS = None
+
+
+def _mx_kinds():
+    """Tensor dtypes accepted for each kind of operand."""
+    global _MX_KINDS
+    if _MX_KINDS is None:
+        import torch
+        extra = lambda name: {getattr(torch, name)} if hasattr(torch, name) else set()  # noqa: E731
+        raw16 = {torch.int16} | extra("uint16")
+        _MX_KINDS = {"f32": {torch.float32}, "bf16": {torch.bfloat16} | raw16,
+                     "f16": {torch.float16} | raw16,
+                     "codes": {torch.uint8} | extra("float4_e2m1fn_x2"),
+                     "scales": {torch.uint8} | extra("float8_e8m0fnu")}
+    return _MX_KINDS
+
+
+def _mx_call(name, head, operands, stream, check):
+    """One MXFP4 entry point: `head` its leading integers, `operands` (kind,
+    address or tensor or None, leading dimension) in the C order.  Tensors lie
+    on one device, whose current stream is the default and which is the
+    current device during the call."""
+    import torch
+    args, dev = list(head), None
+    for kind, x, ld in operands:
+        if isinstance(x, torch.Tensor):
+            if not x.is_cuda:
+                raise ValueError("matrix tensors must live on the GPU")
+            if x.dtype not in _mx_kinds()[kind]:
+                raise TypeError(f"{name}: a {kind} operand cannot be a {x.dtype} tensor")
+            at = x.device.index
+            if dev is None:
+                dev = at
+            elif dev != at:
+                raise ValueError(f"{name}: operands on devices {dev} and {at}")
+            x = x.data_ptr() or None
+        elif x is not None:
+            x = _ptr(x)
+        args += (x, ld)
+    fn = getattr(library(), name)
+    if dev is not None and dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    else:
+        st = fn(*args, _stream(stream))
+    return _check(st) if check else st
+
+
+def _mx_quantize(t, R, C, X, ldx, Q, ldq, S, lds, QT, ldqt, ST, ldst, stream, check):
+    return _mx_call(f"gemm_mxfp4_quantize_{t}", (R, C),
+                    ((t, X, ldx), ("codes", Q, ldq), ("scales", S, lds), ("codes", QT, ldqt),
+                     ("scales", ST, ldst)), stream, check)
+
+
+def gemm_mxfp4_quantize_f32(R, C, X, ldx, Q, ldq, S, lds, QT=None, ldqt=0, ST=None, ldst=0,
+                            stream=None, *, check=True) -> int:
+    """X (R x C, float32) to MXFP4: along rows into (Q, S), along columns into
+    (QT, ST), the transposed matrix; either pair may be None."""
+    return _mx_quantize("f32", R, C, X, ldx, Q, ldq, S, lds, QT, ldqt, ST, ldst, stream, check)
+
+
+def gemm_mxfp4_quantize_bf16(R, C, X, ldx, Q, ldq, S, lds, QT=None, ldqt=0, ST=None, ldst=0,
+                             stream=None, *, check=True) -> int:
+    """gemm_mxfp4_quantize_f32 for bfloat16 X."""
+    return _mx_quantize("bf16", R, C, X, ldx, Q, ldq, S, lds, QT, ldqt, ST, ldst, stream, check)
+
+
+def gemm_mxfp4_quantize_f16(R, C, X, ldx, Q, ldq, S, lds, QT=None, ldqt=0, ST=None, ldst=0,
+                            stream=None, *, check=True) -> int:
+    """gemm_mxfp4_quantize_f32 for binary16 X."""
+    return _mx_quantize("f16", R, C, X, ldx, Q, ldq, S, lds, QT, ldqt, ST, ldst, stream, check)
+
+
+def gemm_mxfp4_dequantize_f32(R, C, Q, ldq, S, lds, Y, ldy, stream=None, *, check=True) -> int:
+    """Y (R x C, float32) = the values of the MXFP4 matrix (Q, S)."""
+    return _mx_call("gemm_mxfp4_dequantize_f32", (R, C),
+                    (("codes", Q, ldq), ("scales", S, lds), ("f32", Y, ldy)), stream, check)
+
+
+def gemm_mxfp4_dequantize_bf16(R, C, Q, ldq, S, lds, Y, ldy, stream=None, *, check=True) -> int:
+    """gemm_mxfp4_dequantize_f32 into bfloat16 Y."""
+    return _mx_call("gemm_mxfp4_dequantize_bf16", (R, C),
+                    (("codes", Q, ldq), ("scales", S, lds), ("bf16", Y, ldy)), stream, check)
+
+
+def gemm_mxfp4_dequantize_f16(R, C, Q, ldq, S, lds, Y, ldy, stream=None, *, check=True) -> int:
+    """gemm_mxfp4_dequantize_f32 into binary16 Y."""
+    return _mx_call("gemm_mxfp4_dequantize_f16", (R, C),
+                    (("codes", Q, ldq), ("scales", S, lds), ("f16", Y, ldy)), stream, check)
+
+
+def gemm_mxfp4_f32(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, stream=None, *,
+                   check=True) -> int:
+    """C = A.B^T, A (M x K) and B (N x K) MXFP4 blocked along K, float32 C."""
+    return _mx_call("gemm_mxfp4_f32", (M, N, K),
+                    (("codes", A, lda), ("scales", SA, ldsa), ("codes", B, ldb),
+                     ("scales", SB, ldsb), ("f32", C, ldc)), stream, check)
+
+
+def gemm_mxfp4_bf16(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, stream=None, *,
+                    check=True) -> int:
+    """gemm_mxfp4_f32 with C rounded once, to bfloat16."""
+    return _mx_call("gemm_mxfp4_bf16", (M, N, K),
+                    (("codes", A, lda), ("scales", SA, ldsa), ("codes", B, ldb),
+                     ("scales", SB, ldsb), ("bf16", C, ldc)), stream, check)
+
+
+def gemm_bf16_mxfp4_f32(M, N, K, A, lda, B, ldb, SB, ldsb, C, ldc, stream=None, *,
+                        check=True) -> int:
+    """C = A.B^T, A (M x K) bfloat16, B (N x K) MXFP4 blocked along K, float32 C."""
+    return _mx_call("gemm_bf16_mxfp4_f32", (M, N, K),
+                    (("bf16", A, lda), ("codes", B, ldb), ("scales", SB, ldsb), ("f32", C, ldc)),
+                    stream, check)
+
+
+def gemm_f16_mxfp4_f32(M, N, K, A, lda, B, ldb, SB, ldsb, C, ldc, stream=None, *,
+                       check=True) -> int:
+    """gemm_bf16_mxfp4_f32 with binary16 A."""
+    return _mx_call("gemm_f16_mxfp4_f32", (M, N, K),
+                    (("f16", A, lda), ("codes", B, ldb), ("scales", SB, ldsb), ("f32", C, ldc)),
+                    stream, check)
 
 
 def matmul(A, B, out=None, path=PATH_AUTO, stream=None):

@@ -1,0 +1,448 @@
+// mxfp4_cast.hip -- quantising a matrix to MXFP4 along its rows, its columns
+// or both, and reading MXFP4 back.
+//
+// For a block x_0 .. x_31 with largest magnitude t:
+//     s = max(floor(log2 t) - 2, -127),  q_i = E2M1(x_i 2^-s)
+// to nearest, ties to even, saturating at 6 (the specification's rule: 2 is
+// the exponent of E2M1's largest value).  The magnitudes' bit patterns order
+// as the magnitudes do, NaN and infinities above all others, so t is an
+// integer maximum; as a float's bits, t's exponent field less 2 is the scale
+// byte, and a field of 255 (NaN or infinity in the block) is itself the byte
+// of a NaN block.  v_cvt_scalef32_pk_fp4_* then divides by 2^s, rounds and
+// saturates exactly so.
+//
+// Everything here is bound by memory: two or four bytes read and about half a
+// byte written per element and direction.
+#include "mxfp4.h"
+
+namespace sgemm {
+namespace {
+
+typedef unsigned short mx_us2 __attribute__((ext_vector_type(2)));
+
+// Eight consecutive elements in a lane's registers, by type: loads (guarded:
+// the first n elements exist, the others are 0), the magnitudes' maximum as
+// float bits, and conversion of pairs.
+template <MxType T>
+struct Eight;
+
+template <>
+struct Eight<MxType::f32> {
+    static constexpr int SIZE = 4;
+    unsigned w[8];
+    template <bool VEC>
+    __device__ __forceinline__ void load(const void* base, long long at, int n) {
+        const unsigned* p = static_cast<const unsigned*>(base) + at;
+        if (VEC && n >= 8) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 4);
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+            w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = i < n ? p[i] : 0u;
+        }
+    }
+    // Running maxima of magnitudes, one per column (COLS) or over all eight.
+    struct Max {
+        unsigned m[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        __device__ __forceinline__ void take(const Eight& x) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = max(m[i], x.w[i] & 0x7FFFFFFFu);
+        }
+        template <int MASK>
+        __device__ __forceinline__ void across() {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], MASK, 64));
+        }
+        __device__ __forceinline__ unsigned bits(int i) const { return m[i]; }
+    };
+    // The largest magnitude of the eight, in a form that maxima of several
+    // lanes are taken in, and that form's float bits.
+    __device__ __forceinline__ unsigned top() const {
+        unsigned m = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+        return m;
+    }
+    static __device__ __forceinline__ unsigned top_bits(unsigned m) { return m; }
+    // Codes of the eight, the first in the lowest four bits.
+    __device__ __forceinline__ unsigned codes(float s) const {
+        unsigned q = 0u;
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f(0), f(1), s, 0);
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f(2), f(3), s, 1);
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f(4), f(5), s, 2);
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f(6), f(7), s, 3);
+    }
+    // Codes of element i of four rows, the first row's in the lowest bits.
+    static __device__ __forceinline__ unsigned column(const Eight (&x)[4], int i, float s) {
+        unsigned q = 0u;
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x[0].f(i), x[1].f(i), s, 0);
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x[2].f(i), x[3].f(i), s, 1);
+    }
+    __device__ __forceinline__ float f(int i) const { return __uint_as_float(w[i]); }
+};
+
+// bf16 and f16: pairs in a register; magnitudes compare as 15-bit integers.
+template <MxType T>
+struct Eight {
+    static constexpr int SIZE = 2;
+    unsigned w[4];
+    template <bool VEC>
+    __device__ __forceinline__ void load(const void* base, long long at, int n) {
+        const unsigned short* p = static_cast<const unsigned short*>(base) + at;
+        if (VEC && n >= 8) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = (2 * i < n ? (unsigned)p[2 * i] : 0u) |
+                       (2 * i + 1 < n ? (unsigned)p[2 * i + 1] : 0u) << 16;
+        }
+    }
+    static __device__ __forceinline__ unsigned pk_max(unsigned a, unsigned b) {
+        return __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(mx_us2, a),
+                                                                      __builtin_bit_cast(mx_us2, b)));
+    }
+    static __device__ __forceinline__ unsigned float_bits(unsigned h) {
+        if constexpr (T == MxType::bf16) return h << 16;
+        else return __float_as_uint((float)__builtin_bit_cast(mx_h2, h)[0]);
+    }
+    struct Max {
+        unsigned m[4] = {0u, 0u, 0u, 0u};
+        __device__ __forceinline__ void take(const Eight& x) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = pk_max(m[i], x.w[i] & 0x7FFF7FFFu);
+        }
+        template <int MASK>
+        __device__ __forceinline__ void across() {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = pk_max(m[i], (unsigned)__shfl_xor((int)m[i], MASK, 64));
+        }
+        __device__ __forceinline__ unsigned bits(int i) const {
+            return float_bits(i & 1 ? m[i / 2] >> 16 : m[i / 2] & 0xFFFFu);
+        }
+    };
+    __device__ __forceinline__ unsigned top() const {
+        const unsigned m = pk_max(pk_max(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                  pk_max(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+        return max(m & 0xFFFFu, m >> 16);
+    }
+    static __device__ __forceinline__ unsigned top_bits(unsigned m) { return float_bits(m); }
+    template <int SEL>
+    static __device__ __forceinline__ unsigned pair(unsigned q, unsigned v, float s) {
+        if constexpr (T == MxType::bf16)
+            return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(mx_bf2, v), s, SEL);
+        else
+            return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(q, __builtin_bit_cast(mx_h2, v), s, SEL);
+    }
+    __device__ __forceinline__ unsigned codes(float s) const {
+        unsigned q = 0u;
+        static_for<4>([&](auto i) { q = pair<i>(q, w[i], s); });
+        return q;
+    }
+    static __device__ __forceinline__ unsigned column(const Eight (&x)[4], int i, float s) {
+        const unsigned sel = i & 1 ? 0x07060302u : 0x05040100u;   // high or low halves of two rows
+        const unsigned q = pair<0>(0u, __builtin_amdgcn_perm(x[1].w[i / 2], x[0].w[i / 2], sel), s);
+        return pair<1>(q, __builtin_amdgcn_perm(x[3].w[i / 2], x[2].w[i / 2], sel), s);
+    }
+};
+
+// Scale byte from the float bits of a block's largest magnitude.
+__device__ __forceinline__ unsigned scale_byte(unsigned bits) {
+    const unsigned e = bits >> 23;
+    return e == 255u ? 255u : max(e, 2u) - 2u;
+}
+
+// Store of the first n (1 .. 4) bytes of q.
+template <bool VEC>
+__device__ __forceinline__ void store_bytes(unsigned char* p, unsigned q, int n) {
+    if (VEC && n >= 4) {
+        *reinterpret_cast<unsigned*>(p) = q;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = (unsigned char)(q >> (8 * i));
+    }
+}
+
+constexpr int kCastItems = 4;   // items a wave has in flight
+
+// Quantising along rows.  A lane holds 8 consecutive elements, four lanes a
+// block, a wave's lanes one row's segment of 8 << LPR elements or, where rows
+// are short, several rows' (lpr: log2 of lanes per row).  Items (segments of
+// row groups) are numbered along the rows; a wave takes four neighbours at a
+// time and loads them all before it converts the first.
+template <MxType T, bool VEC>
+__global__ __launch_bounds__(256) void mx_quantize_rows_kernel(MxQuantArgs p, int lpr, unsigned segs,
+                                                               long long items) {
+    const int lane = threadIdx.x & 63;
+    const int rows_per = 64 >> lpr;
+    const int sub = lane >> lpr, unit = lane & ((1 << lpr) - 1);
+    const long long wave = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const long long waves = (long long)gridDim.x * 4;
+    for (long long first = wave * kCastItems; first < items; first += waves * kCastItems) {
+        Eight<T> x[kCastItems];
+        long long row[kCastItems];
+        int col[kCastItems];
+#pragma unroll
+        for (int u = 0; u < kCastItems; ++u) {
+            const unsigned long long item = first + u;
+            const unsigned long long group =
+                items <= 0xFFFFFFFFll ? (unsigned)item / segs : item / segs;
+            const unsigned seg = (unsigned)(item - group * segs);
+            row[u] = (long long)group * rows_per + sub;
+            // (a segment's start stays below C, so an int holds it; in the
+            // last segment lanes past the row's end could pass 2^31)
+            const long long c = ((long long)seg << lpr) * 8 + unit * 8;
+            const bool in = first + u < items && row[u] < p.R && c < p.C;
+            col[u] = in ? (int)c : -1;
+            x[u].template load<VEC>(p.X, in ? row[u] * p.ldx + c : 0, in ? min(p.C - (int)c, 8) : 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kCastItems; ++u) {
+            unsigned m = x[u].top();
+            m = max(m, (unsigned)__shfl_xor((int)m, 1, 64));
+            m = max(m, (unsigned)__shfl_xor((int)m, 2, 64));
+            const unsigned byte = scale_byte(Eight<T>::top_bits(m));
+            const unsigned q = x[u].codes(mx_scale(byte));
+            if (col[u] < 0) continue;
+            store_bytes<VEC>(p.Q + row[u] * p.ldq + col[u] / 2, q, (min(p.C - col[u], 8) + 1) / 2);
+            if ((lane & 3) == 0) p.S[row[u] * p.lds + col[u] / 32] = (unsigned char)byte;
+        }
+    }
+}
+
+// Quantising along columns, and along rows too where ROWS, in one pass.  A
+// workgroup owns a TILE x TILE piece; each wave takes 32 rows of it (one block
+// of every column), 64 columns at a time: lane l holds rows 4 (l / 8) .. + 3,
+// columns 8 (l % 8) .. + 7.  A row's blocks are quads of lanes; a column's
+// block is the lanes of equal l % 8.  The transposed codes, 2 bytes per lane
+// and column, and scales are gathered in LDS and leave as whole segments down
+// the columns.
+constexpr int kTile = 128;
+constexpr int kTilePitch = kTile / 2 + 4;   // LDS bytes of a column's codes: odd in words
+
+template <MxType T, bool VEC, bool ROWS>
+__global__ __launch_bounds__(256) void mx_quantize_both_kernel(MxQuantArgs p, int tiles_m, int tiles_n) {
+    __shared__ __attribute__((aligned(16))) unsigned char qt[kTile * kTilePitch];
+    __shared__ unsigned st[kTile];
+    int tm, tn;
+    tile_coords(blockIdx.x, tiles_m, tiles_n, 8, p.xcds, tm, tn);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int rg = lane >> 3, cg = lane & 7;
+    const long long r0 = (long long)tm * kTile, c0 = (long long)tn * kTile;
+    const long long r = r0 + wave * 32 + rg * 4;
+#pragma unroll
+    for (int half = 0; half < kTile / 64; ++half) {
+        const long long c = c0 + half * 64 + cg * 8;
+        const int n = (int)max(0ll, min((long long)p.C - c, 8ll));
+        Eight<T> x[4];
+        typename Eight<T>::Max cols;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = r + i < p.R && n > 0;
+            x[i].template load<VEC>(p.X, in ? (r + i) * p.ldx + c : 0, in ? n : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cols.take(x[i]);
+        if constexpr (ROWS) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                unsigned m = x[i].top();
+                m = max(m, (unsigned)__shfl_xor((int)m, 1, 64));
+                m = max(m, (unsigned)__shfl_xor((int)m, 2, 64));
+                const unsigned byte = scale_byte(Eight<T>::top_bits(m));
+                const unsigned q = x[i].codes(mx_scale(byte));
+                if (r + i < p.R && n > 0) {
+                    store_bytes<VEC>(p.Q + (r + i) * p.ldq + c / 2, q, (n + 1) / 2);
+                    if ((lane & 3) == 0) p.S[(r + i) * p.lds + c / 32] = (unsigned char)byte;
+                }
+            }
+        }
+        cols.template across<8>();
+        cols.template across<16>();
+        cols.template across<32>();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned byte = scale_byte(cols.bits(i));
+            const unsigned q = Eight<T>::column(x, i, mx_scale(byte));
+            const int col = half * 64 + cg * 8 + i;
+            *reinterpret_cast<unsigned short*>(&qt[col * kTilePitch + wave * 16 + rg * 2]) = (unsigned short)q;
+            if (rg == i) reinterpret_cast<unsigned char*>(&st[col])[wave] = (unsigned char)byte;
+        }
+    }
+    __syncthreads();
+    // Bytes and scales of this tile that exist down a column.
+    const int rows = (int)min((long long)p.R - r0, (long long)kTile);
+    const int nbytes = (rows + 1) / 2, nscales = (rows + 31) / 32;
+#pragma unroll
+    for (int k = 0; k < kTile * 4 / 256; ++k) {
+        const int id = threadIdx.x + 256 * k, col = id >> 2, at = (id & 3) * 16;
+        if (c0 + col >= p.C) continue;
+        const unsigned* w = reinterpret_cast<const unsigned*>(&qt[col * kTilePitch + at]);
+        unsigned char* out = p.QT + (c0 + col) * p.ldqt + r0 / 2 + at;
+        if (VEC && at + 16 <= nbytes) {
+            *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (at + 4 * j < nbytes) store_bytes<VEC>(out + 4 * j, w[j], min(nbytes - at - 4 * j, 4));
+        }
+    }
+    if (threadIdx.x < kTile && c0 + threadIdx.x < p.C)
+        store_bytes<false>(p.ST + (c0 + threadIdx.x) * p.ldst + r0 / 32, st[threadIdx.x], nscales);
+}
+
+template <MxType T, bool VEC>
+hipError_t quantize_t(const MxQuantArgs& a, hipStream_t s) {
+    if (a.QT != nullptr) {
+        const long long tm = ((long long)a.R + kTile - 1) / kTile, tn = ((long long)a.C + kTile - 1) / kTile;
+        if (tm * tn * 256 > 0xFFFFFFFFll) return hipErrorInvalidValue;
+        if (a.Q != nullptr)
+            mx_quantize_both_kernel<T, VEC, true><<<(unsigned)(tm * tn), 256, 0, s>>>(a, (int)tm, (int)tn);
+        else
+            mx_quantize_both_kernel<T, VEC, false><<<(unsigned)(tm * tn), 256, 0, s>>>(a, (int)tm, (int)tn);
+        return hipGetLastError();
+    }
+    const long long units = ((long long)a.C + 31) / 32 * 4;
+    int lpr = 2;
+    while (lpr < 6 && (1 << lpr) < units) ++lpr;
+    const long long segs = (units + (1 << lpr) - 1) >> lpr;
+    const long long groups = ((long long)a.R + (64 >> lpr) - 1) / (64 >> lpr);
+    const long long items = segs * groups, per_wg = 4 * kCastItems;
+    const long long want = (items + per_wg - 1) / per_wg;
+    const unsigned grid = (unsigned)(want < (1 << 20) ? want : (1 << 20));
+    mx_quantize_rows_kernel<T, VEC><<<grid, 256, 0, s>>>(a, lpr, (unsigned)segs, items);
+    return hipGetLastError();
+}
+
+template <MxType T>
+hipError_t quantize_v(const MxQuantArgs& a, hipStream_t s) {
+    constexpr int e = Eight<T>::SIZE;
+    const bool vec = mx_aligned(a.X, a.ldx * e, 16) && (a.Q == nullptr || mx_aligned(a.Q, a.ldq, 4)) &&
+                     (a.QT == nullptr || mx_aligned(a.QT, a.ldqt, 16));
+    return vec ? quantize_t<T, true>(a, s) : quantize_t<T, false>(a, s);
+}
+
+// Reading back: a lane takes 8 codes (4 bytes), lanes and items as in the
+// row quantiser.
+template <MxType T, bool VEC>
+__global__ __launch_bounds__(256) void mx_dequantize_kernel(MxDequantArgs p, int lpr, unsigned segs,
+                                                            long long items) {
+    const int lane = threadIdx.x & 63;
+    const int rows_per = 64 >> lpr;
+    const int sub = lane >> lpr, unit = lane & ((1 << lpr) - 1);
+    const long long wave = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const long long waves = (long long)gridDim.x * 4;
+    for (long long first = wave * kCastItems; first < items; first += waves * kCastItems) {
+        unsigned q[kCastItems], byte[kCastItems];
+        long long row[kCastItems];
+        int col[kCastItems];
+#pragma unroll
+        for (int u = 0; u < kCastItems; ++u) {
+            const unsigned long long item = first + u;
+            const unsigned long long group =
+                items <= 0xFFFFFFFFll ? (unsigned)item / segs : item / segs;
+            const unsigned seg = (unsigned)(item - group * segs);
+            row[u] = (long long)group * rows_per + sub;
+            const long long c = ((long long)seg << lpr) * 8 + unit * 8;
+            const bool in = first + u < items && row[u] < p.R && c < p.C;
+            col[u] = in ? (int)c : -1;
+            q[u] = 0u;
+            byte[u] = 0u;
+            if (!in) continue;
+            const unsigned char* src = p.Q + row[u] * p.ldq + c / 2;
+            if (VEC && p.C - c >= 8) {
+                q[u] = *reinterpret_cast<const unsigned*>(src);
+            } else {
+                const int n = (min(p.C - (int)c, 8) + 1) / 2;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < n) q[u] |= (unsigned)src[i] << (8 * i);
+            }
+            byte[u] = p.S[row[u] * p.lds + c / 32];
+        }
+#pragma unroll
+        for (int u = 0; u < kCastItems; ++u) {
+            if (col[u] < 0) continue;
+            const float s = mx_scale(byte[u]);
+            const int n = min(p.C - col[u], 8);
+            float v[8];
+            static_for<4>([&](auto i) {
+                const mx_f2 t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, i);
+                v[2 * i] = t.x;
+                v[2 * i + 1] = t.y;
+            });
+            const long long at = row[u] * p.ldy + col[u];
+            if constexpr (T == MxType::f32) {
+                float* y = static_cast<float*>(p.Y) + at;
+                if (VEC && n == 8) {
+                    *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4*>(y + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < n) y[i] = v[i];
+                }
+            } else {
+                // bf16: every value is one of bf16's own, its float's upper
+                // half (four significant bits at most; a NaN stays one).
+                // f16: rounded from the exact float.
+                unsigned short h[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    h[i] = T == MxType::bf16 ? (unsigned short)(__float_as_uint(v[i]) >> 16)
+                                             : __builtin_bit_cast(unsigned short, (_Float16)v[i]);
+                unsigned short* y = static_cast<unsigned short*>(p.Y) + at;
+                if (VEC && n == 8) {
+                    *reinterpret_cast<uint4*>(y) =
+                        make_uint4(h[0] | (unsigned)h[1] << 16, h[2] | (unsigned)h[3] << 16,
+                                   h[4] | (unsigned)h[5] << 16, h[6] | (unsigned)h[7] << 16);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < n) y[i] = h[i];
+                }
+            }
+        }
+    }
+}
+
+template <MxType T>
+hipError_t dequantize_v(const MxDequantArgs& a, hipStream_t s) {
+    const long long units = ((long long)a.C + 31) / 32 * 4;
+    int lpr = 2;
+    while (lpr < 6 && (1 << lpr) < units) ++lpr;
+    const long long segs = (units + (1 << lpr) - 1) >> lpr;
+    const long long groups = ((long long)a.R + (64 >> lpr) - 1) / (64 >> lpr);
+    const long long items = segs * groups, per_wg = 4 * kCastItems;
+    const long long want = (items + per_wg - 1) / per_wg;
+    const unsigned grid = (unsigned)(want < (1 << 20) ? want : (1 << 20));
+    const bool vec = mx_aligned(a.Q, a.ldq, 4) && mx_aligned(a.Y, a.ldy * Eight<T>::SIZE, 16);
+    if (vec)
+        mx_dequantize_kernel<T, true><<<grid, 256, 0, s>>>(a, lpr, (unsigned)segs, items);
+    else
+        mx_dequantize_kernel<T, false><<<grid, 256, 0, s>>>(a, lpr, (unsigned)segs, items);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const MxQuantArgs& a, MxType t, hipStream_t s) {
+    switch (t) {
+        case MxType::f32: return quantize_v<MxType::f32>(a, s);
+        case MxType::bf16: return quantize_v<MxType::bf16>(a, s);
+        default: return quantize_v<MxType::f16>(a, s);
+    }
+}
+
+hipError_t launch_mx_dequantize(const MxDequantArgs& a, MxType t, hipStream_t s) {
+    switch (t) {
+        case MxType::f32: return dequantize_v<MxType::f32>(a, s);
+        case MxType::bf16: return dequantize_v<MxType::bf16>(a, s);
+        default: return dequantize_v<MxType::f16>(a, s);
+    }
+}
+
+}  // namespace sgemm
