@@ -274,20 +274,36 @@ def _mx_kinds():
     return _MX_KINDS
 
 
+_torch = None
+_raw_stream = None
+
+
+def _mx_setup():
+    """torch, and its call for the current stream's handle on a device."""
+    global _torch, _raw_stream
+    import torch
+    _mx_kinds()
+    _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                   or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+    _torch = torch
+
+
 def _mx_call(name, head, operands, stream, check):
     """One MXFP4 entry point: `head` its leading integers, `operands` (kind,
     address or tensor or None, leading dimension) in the C order.  Tensors lie
     on one device, whose current stream is the default and which is the
     current device during the call."""
-    import torch
+    if _torch is None:
+        _mx_setup()
+    tensor = _torch.Tensor
     args, dev = list(head), None
     for kind, x, ld in operands:
-        if isinstance(x, torch.Tensor):
+        if isinstance(x, tensor):
+            if x.dtype not in _MX_KINDS[kind]:
+                raise TypeError(f"{name}: a {kind} operand cannot be a {x.dtype} tensor")
             if not x.is_cuda:
                 raise ValueError("matrix tensors must live on the GPU")
-            if x.dtype not in _mx_kinds()[kind]:
-                raise TypeError(f"{name}: a {kind} operand cannot be a {x.dtype} tensor")
-            at = x.device.index
+            at = x.get_device()
             if dev is None:
                 dev = at
             elif dev != at:
@@ -295,11 +311,14 @@ def _mx_call(name, head, operands, stream, check):
             x = x.data_ptr() or None
         elif x is not None:
             x = _ptr(x)
-        args += (x, ld)
-    fn = getattr(library(), name)
-    if dev is not None and dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream))
+        args.append(x)
+        args.append(ld)
+    fn = getattr(_lib or library(), name)
+    if dev is not None and dev != _torch.cuda.current_device():
+        with _torch.cuda.device(dev):
+            st = fn(*args, (_raw_stream(dev) or None) if stream is None else _stream(stream))
+    elif dev is not None and stream is None:
+        st = fn(*args, _raw_stream(dev) or None)
     else:
         st = fn(*args, _stream(stream))
     return _check(st) if check else st

@@ -123,7 +123,7 @@ __device__ __forceinline__ uint4 mx_codes16(const unsigned char* row, long long 
     return v;
 }
 
-// N (4 or 8) scale bytes from byte `at` of a row of n: zeros past n.
+// N (4, 8 or 16) scale bytes from byte `at` of a row of n: zeros past n.
 template <int N>
 __device__ __forceinline__ void mx_scales(const unsigned char* row, long long at, long long n,
                                           unsigned (&s)[N / 4]) {
@@ -136,6 +136,33 @@ __device__ __forceinline__ void mx_scales(const unsigned char* row, long long at
         for (int i = 0; i < N; ++i)
             if (i < n - at) s[i / 4] |= (unsigned)row[at + i] << (8 * (i % 4));
     }
+}
+
+// A block's 16 bytes of codes without elements `left` and up (left may be
+// negative or past 32).
+__device__ __forceinline__ uint4 mx_keep(uint4 v, int left) {
+    auto word = [&](unsigned w, int i) {
+        const int n = left - 8 * i;
+        return n >= 8 ? w : n <= 0 ? 0u : w & ((1u << (4 * n)) - 1u);
+    };
+    return make_uint4(word(v.x, 0), word(v.y, 1), word(v.z, 2), word(v.w, 3));
+}
+
+// The DMA loaders address a tile's rows by 32-bit offsets from its first row.
+inline bool mx_dma_reach(long long ld_bytes, int rows) { return ld_bytes * rows < (1ll << 32); }
+
+// Four registers, each holding in lane group t (of 16 lanes) what groups 0 to
+// 3 need for tile t; afterwards register t holds in lane group g what group g
+// needs for tile t: a transpose across the lane groups.
+__device__ __forceinline__ void mx_transpose4(unsigned (&d)[4]) {
+    const auto a = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
+    const auto x = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    d[0] = x[0];
+    d[1] = x[1];
+    d[2] = y[0];
+    d[3] = y[1];
 }
 #endif
 }  // namespace sgemm

@@ -20,6 +20,30 @@ namespace {
 
 typedef unsigned short mx_us2 __attribute__((ext_vector_type(2)));
 
+// f(v, the value of lane ^ MASK) for every lane, f symmetric: by the data
+// paths between lanes of a quad and of a row of 16, and by exchanging rows.
+template <int MASK, class F>
+__device__ __forceinline__ unsigned with_lane_xor(unsigned v, F&& f) {
+    if constexpr (MASK == 1 || MASK == 2) {
+        constexpr int quad = MASK == 1 ? 0xB1 : 0x4E;   // quad_perm [1,0,3,2] / [2,3,0,1]
+        return f(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, quad, 0xF, 0xF, true));
+    } else if constexpr (MASK == 8) {
+        return f(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true));   // row_ror:8
+    } else if constexpr (MASK == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return f(r[0], r[1]);
+    } else {
+        static_assert(MASK == 32, "lane exchanges that are used");
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return f(r[0], r[1]);
+    }
+}
+__device__ __forceinline__ unsigned max_of(unsigned a, unsigned b) { return max(a, b); }
+// The largest over a quad of lanes.
+__device__ __forceinline__ unsigned quad_max(unsigned v) {
+    return with_lane_xor<2>(with_lane_xor<1>(v, max_of), max_of);
+}
+
 // Eight consecutive elements in a lane's registers, by type: loads (guarded:
 // the first n elements exist, the others are 0), the magnitudes' maximum as
 // float bits, and conversion of pairs.
@@ -52,7 +76,7 @@ struct Eight<MxType::f32> {
         template <int MASK>
         __device__ __forceinline__ void across() {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m[i] = max(m[i], (unsigned)__shfl_xor((int)m[i], MASK, 64));
+            for (int i = 0; i < 8; ++i) m[i] = with_lane_xor<MASK>(m[i], max_of);
         }
         __device__ __forceinline__ unsigned bits(int i) const { return m[i]; }
     };
@@ -117,7 +141,7 @@ struct Eight {
         template <int MASK>
         __device__ __forceinline__ void across() {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = pk_max(m[i], (unsigned)__shfl_xor((int)m[i], MASK, 64));
+            for (int i = 0; i < 4; ++i) m[i] = with_lane_xor<MASK>(m[i], pk_max);
         }
         __device__ __forceinline__ unsigned bits(int i) const {
             return float_bits(i & 1 ? m[i / 2] >> 16 : m[i / 2] & 0xFFFFu);
@@ -168,6 +192,27 @@ __device__ __forceinline__ void store_bytes(unsigned char* p, unsigned q, int n)
 
 constexpr int kCastItems = 4;   // items a wave has in flight
 
+// How R rows of C elements, E to a lane and a block's lanes together, are
+// divided: log2 of the lanes a row gets, segments of that many lanes in a row,
+// items (a segment of one row group) and workgroups of four waves that take
+// `at_a_time` items each.
+struct Items {
+    int lpr;
+    unsigned segs, grid;
+    long long items;
+};
+Items items_of(int R, int C, int E, int at_a_time) {
+    const long long units = ((long long)C + 31) / 32 * (32 / E);
+    Items it;
+    it.lpr = E == 8 ? 2 : 3;
+    while (it.lpr < 6 && (1 << it.lpr) < units) ++it.lpr;
+    it.segs = (unsigned)((units + (1 << it.lpr) - 1) >> it.lpr);
+    it.items = it.segs * (((long long)R + (64 >> it.lpr) - 1) / (64 >> it.lpr));
+    const long long want = (it.items + 4 * at_a_time - 1) / (4 * at_a_time);
+    it.grid = (unsigned)(want < (1 << 20) ? want : (1 << 20));
+    return it;
+}
+
 // Quantising along rows.  A lane holds 8 consecutive elements, four lanes a
 // block, a wave's lanes one row's segment of 8 << LPR elements or, where rows
 // are short, several rows' (lpr: log2 of lanes per row).  Items (segments of
@@ -201,9 +246,7 @@ __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(MxQuantArgs p, in
         }
 #pragma unroll
         for (int u = 0; u < kCastItems; ++u) {
-            unsigned m = x[u].top();
-            m = max(m, (unsigned)__shfl_xor((int)m, 1, 64));
-            m = max(m, (unsigned)__shfl_xor((int)m, 2, 64));
+            const unsigned m = quad_max(x[u].top());
             const unsigned byte = scale_byte(Eight<T>::top_bits(m));
             const unsigned q = x[u].codes(mx_scale(byte));
             if (col[u] < 0) continue;
@@ -220,21 +263,26 @@ __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(MxQuantArgs p, in
 // block is the lanes of equal l % 8.  The transposed codes, 2 bytes per lane
 // and column, and scales are gathered in LDS and leave as whole segments down
 // the columns.
-constexpr int kTile = 128;
-constexpr int kTilePitch = kTile / 2 + 4;   // LDS bytes of a column's codes: odd in words
+#ifndef TR
+#define TR 128
+#define TC 128
+#endif
+constexpr int kTileR = TR, kTileC = TC;
+constexpr int kTileWaves = kTileR / 32;
+constexpr int kTilePitch = kTileR / 2 + 4;   // LDS bytes of a column's codes: odd in words
 
 template <MxType T, bool VEC, bool ROWS>
-__global__ __launch_bounds__(256) void mx_quantize_both_kernel(MxQuantArgs p, int tiles_m, int tiles_n) {
-    __shared__ __attribute__((aligned(16))) unsigned char qt[kTile * kTilePitch];
-    __shared__ unsigned st[kTile];
+__global__ __launch_bounds__(64 * kTileWaves) void mx_quantize_both_kernel(MxQuantArgs p, int tiles_m, int tiles_n) {
+    __shared__ __attribute__((aligned(16))) unsigned char qt[kTileC * kTilePitch];
+    __shared__ __attribute__((aligned(16))) unsigned char st[kTileC * kTileWaves];
     int tm, tn;
     tile_coords(blockIdx.x, tiles_m, tiles_n, 8, p.xcds, tm, tn);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int rg = lane >> 3, cg = lane & 7;
-    const long long r0 = (long long)tm * kTile, c0 = (long long)tn * kTile;
+    const long long r0 = (long long)tm * kTileR, c0 = (long long)tn * kTileC;
     const long long r = r0 + wave * 32 + rg * 4;
 #pragma unroll
-    for (int half = 0; half < kTile / 64; ++half) {
+    for (int half = 0; half < kTileC / 64; ++half) {
         const long long c = c0 + half * 64 + cg * 8;
         const int n = (int)max(0ll, min((long long)p.C - c, 8ll));
         Eight<T> x[4];
@@ -249,9 +297,7 @@ __global__ __launch_bounds__(256) void mx_quantize_both_kernel(MxQuantArgs p, in
         if constexpr (ROWS) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                unsigned m = x[i].top();
-                m = max(m, (unsigned)__shfl_xor((int)m, 1, 64));
-                m = max(m, (unsigned)__shfl_xor((int)m, 2, 64));
+                const unsigned m = quad_max(x[i].top());
                 const unsigned byte = scale_byte(Eight<T>::top_bits(m));
                 const unsigned q = x[i].codes(mx_scale(byte));
                 if (r + i < p.R && n > 0) {
@@ -269,16 +315,18 @@ __global__ __launch_bounds__(256) void mx_quantize_both_kernel(MxQuantArgs p, in
             const unsigned q = Eight<T>::column(x, i, mx_scale(byte));
             const int col = half * 64 + cg * 8 + i;
             *reinterpret_cast<unsigned short*>(&qt[col * kTilePitch + wave * 16 + rg * 2]) = (unsigned short)q;
-            if (rg == i) reinterpret_cast<unsigned char*>(&st[col])[wave] = (unsigned char)byte;
+            if (rg == i) st[col * kTileWaves + wave] = (unsigned char)byte;
         }
     }
     __syncthreads();
     // Bytes and scales of this tile that exist down a column.
-    const int rows = (int)min((long long)p.R - r0, (long long)kTile);
+    const int rows = (int)min((long long)p.R - r0, (long long)kTileR);
     const int nbytes = (rows + 1) / 2, nscales = (rows + 31) / 32;
+    constexpr int PER = kTileR / 32;             // 16-byte chunks down a column
+    constexpr int NT = 64 * kTileWaves;
 #pragma unroll
-    for (int k = 0; k < kTile * 4 / 256; ++k) {
-        const int id = threadIdx.x + 256 * k, col = id >> 2, at = (id & 3) * 16;
+    for (int k = 0; k < kTileC * PER / NT; ++k) {
+        const int id = threadIdx.x + NT * k, col = id / PER, at = id % PER * 16;
         if (c0 + col >= p.C) continue;
         const unsigned* w = reinterpret_cast<const unsigned*>(&qt[col * kTilePitch + at]);
         unsigned char* out = p.QT + (c0 + col) * p.ldqt + r0 / 2 + at;
@@ -290,30 +338,31 @@ __global__ __launch_bounds__(256) void mx_quantize_both_kernel(MxQuantArgs p, in
                 if (at + 4 * j < nbytes) store_bytes<VEC>(out + 4 * j, w[j], min(nbytes - at - 4 * j, 4));
         }
     }
-    if (threadIdx.x < kTile && c0 + threadIdx.x < p.C)
-        store_bytes<false>(p.ST + (c0 + threadIdx.x) * p.ldst + r0 / 32, st[threadIdx.x], nscales);
+    for (int col = threadIdx.x; col < kTileC && c0 + col < p.C; col += NT) {
+        unsigned char* out = p.ST + (c0 + col) * p.ldst + r0 / 32;
+        const unsigned char* in = &st[col * kTileWaves];
+        if (nscales == kTileWaves) {
+            __builtin_memcpy(out, in, kTileWaves);   // any alignment
+        } else {
+            for (int i = 0; i < nscales; ++i) out[i] = in[i];
+        }
+    }
 }
 
 template <MxType T, bool VEC>
 hipError_t quantize_t(const MxQuantArgs& a, hipStream_t s) {
     if (a.QT != nullptr) {
-        const long long tm = ((long long)a.R + kTile - 1) / kTile, tn = ((long long)a.C + kTile - 1) / kTile;
-        if (tm * tn * 256 > 0xFFFFFFFFll) return hipErrorInvalidValue;
+        const long long tm = ((long long)a.R + kTileR - 1) / kTileR, tn = ((long long)a.C + kTileC - 1) / kTileC;
+        constexpr int NT = 64 * kTileWaves;
+        if (tm * tn * NT > 0xFFFFFFFFll) return hipErrorInvalidValue;
         if (a.Q != nullptr)
-            mx_quantize_both_kernel<T, VEC, true><<<(unsigned)(tm * tn), 256, 0, s>>>(a, (int)tm, (int)tn);
+            mx_quantize_both_kernel<T, VEC, true><<<(unsigned)(tm * tn), NT, 0, s>>>(a, (int)tm, (int)tn);
         else
-            mx_quantize_both_kernel<T, VEC, false><<<(unsigned)(tm * tn), 256, 0, s>>>(a, (int)tm, (int)tn);
+            mx_quantize_both_kernel<T, VEC, false><<<(unsigned)(tm * tn), NT, 0, s>>>(a, (int)tm, (int)tn);
         return hipGetLastError();
     }
-    const long long units = ((long long)a.C + 31) / 32 * 4;
-    int lpr = 2;
-    while (lpr < 6 && (1 << lpr) < units) ++lpr;
-    const long long segs = (units + (1 << lpr) - 1) >> lpr;
-    const long long groups = ((long long)a.R + (64 >> lpr) - 1) / (64 >> lpr);
-    const long long items = segs * groups, per_wg = 4 * kCastItems;
-    const long long want = (items + per_wg - 1) / per_wg;
-    const unsigned grid = (unsigned)(want < (1 << 20) ? want : (1 << 20));
-    mx_quantize_rows_kernel<T, VEC><<<grid, 256, 0, s>>>(a, lpr, (unsigned)segs, items);
+    const Items it = items_of(a.R, a.C, 8, kCastItems);
+    mx_quantize_rows_kernel<T, VEC><<<it.grid, 256, 0, s>>>(a, it.lpr, it.segs, it.items);
     return hipGetLastError();
 }
 
@@ -325,84 +374,86 @@ hipError_t quantize_v(const MxQuantArgs& a, hipStream_t s) {
     return vec ? quantize_t<T, true>(a, s) : quantize_t<T, false>(a, s);
 }
 
-// Reading back: a lane takes 8 codes (4 bytes), lanes and items as in the
+// Reading back: a lane takes 16 bytes of output -- 4 floats or 8 16-bit values
+// -- so that a wave's stores are whole kilobytes; lanes and items as in the
 // row quantiser.
 template <MxType T, bool VEC>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(MxDequantArgs p, int lpr, unsigned segs,
                                                             long long items) {
+    constexpr int E = T == MxType::f32 ? 4 : 8, ITEMS = 32 / E;
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
     const int lane = threadIdx.x & 63;
     const int rows_per = 64 >> lpr;
     const int sub = lane >> lpr, unit = lane & ((1 << lpr) - 1);
     const long long wave = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const long long waves = (long long)gridDim.x * 4;
-    for (long long first = wave * kCastItems; first < items; first += waves * kCastItems) {
-        unsigned q[kCastItems], byte[kCastItems];
-        long long row[kCastItems];
-        int col[kCastItems];
+    for (long long first = wave * ITEMS; first < items; first += waves * ITEMS) {
+        unsigned q[ITEMS], byte[ITEMS];
+        long long row[ITEMS];
+        int col[ITEMS];
 #pragma unroll
-        for (int u = 0; u < kCastItems; ++u) {
+        for (int u = 0; u < ITEMS; ++u) {
             const unsigned long long item = first + u;
             const unsigned long long group =
                 items <= 0xFFFFFFFFll ? (unsigned)item / segs : item / segs;
             const unsigned seg = (unsigned)(item - group * segs);
             row[u] = (long long)group * rows_per + sub;
-            const long long c = ((long long)seg << lpr) * 8 + unit * 8;
+            const long long c = (((long long)seg << lpr) + unit) * E;
             const bool in = first + u < items && row[u] < p.R && c < p.C;
             col[u] = in ? (int)c : -1;
             q[u] = 0u;
             byte[u] = 0u;
             if (!in) continue;
             const unsigned char* src = p.Q + row[u] * p.ldq + c / 2;
-            if (VEC && p.C - c >= 8) {
-                q[u] = *reinterpret_cast<const unsigned*>(src);
+            if (VEC && p.C - c >= E) {
+                if constexpr (E == 8) q[u] = *reinterpret_cast<const unsigned*>(src);
+                else q[u] = *reinterpret_cast<const unsigned short*>(src);
             } else {
-                const int n = (min(p.C - (int)c, 8) + 1) / 2;
+                const int n = (min(p.C - (int)c, E) + 1) / 2;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < E / 2; ++i)
                     if (i < n) q[u] |= (unsigned)src[i] << (8 * i);
             }
             byte[u] = p.S[row[u] * p.lds + c / 32];
         }
 #pragma unroll
-        for (int u = 0; u < kCastItems; ++u) {
+        for (int u = 0; u < ITEMS; ++u) {
             if (col[u] < 0) continue;
             const float s = mx_scale(byte[u]);
-            const int n = min(p.C - col[u], 8);
-            float v[8];
-            static_for<4>([&](auto i) {
+            const int n = min(p.C - col[u], E);
+            unsigned v[E];
+            static_for<E / 2>([&](auto i) {
                 const mx_f2 t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, i);
-                v[2 * i] = t.x;
-                v[2 * i + 1] = t.y;
+                v[2 * i] = __float_as_uint(t.x);
+                v[2 * i + 1] = __float_as_uint(t.y);
             });
             const long long at = row[u] * p.ldy + col[u];
             if constexpr (T == MxType::f32) {
-                float* y = static_cast<float*>(p.Y) + at;
-                if (VEC && n == 8) {
-                    *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
-                    *reinterpret_cast<float4*>(y + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                unsigned* y = static_cast<unsigned*>(p.Y) + at;
+                if (VEC && n == E) {
+                    __builtin_nontemporal_store(u32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<u32x4*>(y));
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int i = 0; i < E; ++i)
                         if (i < n) y[i] = v[i];
                 }
             } else {
                 // bf16: every value is one of bf16's own, its float's upper
-                // half (four significant bits at most; a NaN stays one).
-                // f16: rounded from the exact float.
-                unsigned short h[8];
+                // half (two significant bits; a NaN stays one).  f16: rounded
+                // from the exact float.
+                unsigned h[E];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    h[i] = T == MxType::bf16 ? (unsigned short)(__float_as_uint(v[i]) >> 16)
-                                             : __builtin_bit_cast(unsigned short, (_Float16)v[i]);
+                for (int i = 0; i < E; ++i)
+                    h[i] = T == MxType::bf16 ? v[i] >> 16
+                                             : __builtin_bit_cast(unsigned short, (_Float16)__uint_as_float(v[i]));
                 unsigned short* y = static_cast<unsigned short*>(p.Y) + at;
-                if (VEC && n == 8) {
-                    *reinterpret_cast<uint4*>(y) =
-                        make_uint4(h[0] | (unsigned)h[1] << 16, h[2] | (unsigned)h[3] << 16,
-                                   h[4] | (unsigned)h[5] << 16, h[6] | (unsigned)h[7] << 16);
+                if (VEC && n == E) {
+                    __builtin_nontemporal_store(u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
+                                                      h[6] | h[7] << 16}, reinterpret_cast<u32x4*>(y));
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < n) y[i] = h[i];
+                    for (int i = 0; i < E; ++i)
+                        if (i < n) y[i] = (unsigned short)h[i];
                 }
             }
         }
@@ -411,19 +462,13 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(MxDequantArgs p, int
 
 template <MxType T>
 hipError_t dequantize_v(const MxDequantArgs& a, hipStream_t s) {
-    const long long units = ((long long)a.C + 31) / 32 * 4;
-    int lpr = 2;
-    while (lpr < 6 && (1 << lpr) < units) ++lpr;
-    const long long segs = (units + (1 << lpr) - 1) >> lpr;
-    const long long groups = ((long long)a.R + (64 >> lpr) - 1) / (64 >> lpr);
-    const long long items = segs * groups, per_wg = 4 * kCastItems;
-    const long long want = (items + per_wg - 1) / per_wg;
-    const unsigned grid = (unsigned)(want < (1 << 20) ? want : (1 << 20));
-    const bool vec = mx_aligned(a.Q, a.ldq, 4) && mx_aligned(a.Y, a.ldy * Eight<T>::SIZE, 16);
+    constexpr int E = T == MxType::f32 ? 4 : 8, ITEMS = 32 / E;
+    const Items it = items_of(a.R, a.C, E, ITEMS);
+    const bool vec = mx_aligned(a.Q, a.ldq, E / 2) && mx_aligned(a.Y, a.ldy * Eight<T>::SIZE, 16);
     if (vec)
-        mx_dequantize_kernel<T, true><<<grid, 256, 0, s>>>(a, lpr, (unsigned)segs, items);
+        mx_dequantize_kernel<T, true><<<it.grid, 256, 0, s>>>(a, it.lpr, it.segs, it.items);
     else
-        mx_dequantize_kernel<T, false><<<grid, 256, 0, s>>>(a, lpr, (unsigned)segs, items);
+        mx_dequantize_kernel<T, false><<<it.grid, 256, 0, s>>>(a, it.lpr, it.segs, it.items);
     return hipGetLastError();
 }
 

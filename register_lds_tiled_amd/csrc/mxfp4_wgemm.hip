@@ -5,9 +5,11 @@
 // -128 and 129, so bfloat16 holds it exactly (2^128 and beyond as infinity):
 // B's codes become bfloat16 in registers (v_cvt_scalef32_pk_bf16_fp4, two
 // elements with their scale) and multiply in v_mfma_f32_16x16x32_bf16.
-// binary16 A: binary16 cannot hold all of B's values, but A splits exactly
-// into two bfloat16 terms, hi + lo (11 significant bits in 8 + 8), and both
-// multiply the same B.
+// binary16 A: where binary16 holds every value of the blocks at hand (scale
+// bytes 104 to 140, any usual weight), they become binary16 and multiply in
+// v_mfma_f32_16x16x32_f16.  Where it does not, A splits exactly into two
+// bfloat16 terms, hi + lo (11 significant bits in 8 + 8), and both multiply
+// the same bfloat16 B.
 //
 // v_mfma_f32_16x16x32_bf16: lane l holds 8 consecutive k of row l % 16 of each
 // operand; D: lane l, register i is row 4 (l / 16) + i of the first operand,
@@ -19,15 +21,19 @@ namespace sgemm {
 namespace {
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 
-// The eight values of four bytes of codes, as bfloat16.
+// The eight values of four bytes of codes: in A's type, or (SPLIT) in bfloat16.
+template <MxType T, bool SPLIT>
 __device__ __forceinline__ uint4 decode8(unsigned q, float s) {
-    uint4 v;
-    v.x = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0));
-    v.y = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1));
-    v.z = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2));
-    v.w = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3));
-    return v;
+    unsigned v[4];
+    static_for<4>([&](auto i) {
+        if constexpr (T == MxType::bf16 || SPLIT)
+            v[i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, i));
+        else
+            v[i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, i));
+    });
+    return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // Two binary16 values as bfloat16 hi and lo with hi + lo their exact sum: hi
@@ -48,13 +54,45 @@ __device__ __forceinline__ mx_f4 mfma_bf16(uint4 b, uint4 a, mx_f4 acc) {
                                                    acc, 0, 0, 0);
 }
 
-__device__ __forceinline__ void store4(const MxGemmArgs& p, long long row, int col, mx_f4 v) {
-    if (row >= p.M || col >= p.N) return;
-    const int n = min(p.N - col, 4);
-    float* c = static_cast<float*>(p.C) + row * p.ldc + col;
+// Whether binary16 holds every value of a block with this scale byte: the
+// smallest, 2^(byte - 128), from its least subnormal 2^-24, the largest,
+// 6 2^(byte - 127), to 65504.
+__device__ __forceinline__ bool f16_holds(unsigned byte) { return byte - 104u <= 36u; }
+
+// acc[j] += a step of 32 k for N tiles of B's rows (decoded by decode8 with
+// the same SPLIT) and one tile of A's.
+template <MxType T, bool SPLIT, int N>
+__device__ __forceinline__ void mfma_row(const uint4 (&b)[N], uint4 a, mx_f4 (&acc)[N]) {
+    if constexpr (T == MxType::bf16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < n) store_c(c + i, v[i]);
+        for (int j = 0; j < N; ++j) acc[j] = mfma_bf16(b[j], a, acc[j]);
+    } else if constexpr (SPLIT) {
+        uint4 hi, lo;
+        split2(a.x, hi.x, lo.x);
+        split2(a.y, hi.y, lo.y);
+        split2(a.z, hi.z, lo.z);
+        split2(a.w, hi.w, lo.w);
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = mfma_bf16(b[j], lo, mfma_bf16(b[j], hi, acc[j]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, b[j]),
+                                                            __builtin_bit_cast(half8, a), acc[j], 0, 0, 0);
+    }
+}
+
+__device__ __forceinline__ void store4(const MxGemmArgs& p, long long row, long long col, mx_f4 v) {
+    if (row >= p.M || col >= p.N) return;
+    const int n = (int)min(p.N - col, 4ll);
+    float* c = static_cast<float*>(p.C) + row * p.ldc + col;
+    if (n == 4 && ((size_t)c & 15) == 0) {
+        store_c4(c, v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) store_c(c + i, v[i]);
+    }
 }
 
 // 16 bytes of A of which the first n exist (n even).
@@ -90,7 +128,7 @@ struct WTile {
 };
 
 template <class Cfg, MxType T, bool VEC>
-__global__ __launch_bounds__(Cfg::NT) void mx_wtile_kernel(MxGemmArgs p, int tiles_m, int tiles_n) {
+__global__ __launch_bounds__(Cfg::NT, 2) void mx_wtile_kernel(MxGemmArgs p, int tiles_m, int tiles_n) {
     constexpr int BM = Cfg::BM, BN = Cfg::BN, NT = Cfg::NT, FM = Cfg::FM, FN = Cfg::FN;
     constexpr int CA = BM * 16 / NT, CB = BN * 4 / NT;
     static_assert(BM * 16 % NT == 0 && BN * 4 % NT == 0 && BN <= NT, "whole rounds of the loader");
@@ -148,39 +186,36 @@ __global__ __launch_bounds__(Cfg::NT) void mx_wtile_kernel(MxGemmArgs p, int til
             q[j] = bs[r * 4 + (g ^ ((r >> 1) & 3))];
             sb[j] = mx_scale((sc[r] >> (8 * g)) & 255u);
         }
-        static_for<4>([&](auto t) {
-            uint4 b[FN];
+        bool in_range = true;
+        if constexpr (T == MxType::f16) {
+            bool ok = true;
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const unsigned w = t == 0 ? q[j].x : t == 1 ? q[j].y : t == 2 ? q[j].z : q[j].w;
-                b[j] = decode8(w, sb[j]);
-            }
+            for (int j = 0; j < FN; ++j) ok = ok && f16_holds(__float_as_uint(sb[j]) >> 23);
+            in_range = __all(ok);
+        }
+        auto steps = [&](auto split) {
+            static_for<4>([&](auto t) {
+                uint4 b[FN];
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const uint4 a = as[(wm + 16 * i + li) * 16 + ((4 * g + t) ^ li)];
-                if constexpr (T == MxType::bf16) {
+                for (int j = 0; j < FN; ++j)
+                    b[j] = decode8<T, split>(t == 0 ? q[j].x : t == 1 ? q[j].y : t == 2 ? q[j].z : q[j].w, sb[j]);
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) acc[i][j] = mfma_bf16(b[j], a, acc[i][j]);
-                } else {
-                    uint4 hi, lo;
-                    split2(a.x, hi.x, lo.x);
-                    split2(a.y, hi.y, lo.y);
-                    split2(a.z, hi.z, lo.z);
-                    split2(a.w, hi.w, lo.w);
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) {
-                        acc[i][j] = mfma_bf16(b[j], hi, acc[i][j]);
-                        acc[i][j] = mfma_bf16(b[j], lo, acc[i][j]);
-                    }
+                for (int i = 0; i < FM; ++i) {
+                    const uint4 a = as[(wm + 16 * i + li) * 16 + ((4 * g + t) ^ li)];
+                    mfma_row<T, split, FN>(b, a, acc[i]);
                 }
-            }
-        });
+            });
+        };
+        if (in_range)
+            steps(std::false_type{});
+        else
+            steps(std::true_type{});
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-            store4(p, m0 + wm + 16 * i + li, (int)(n0 + wn + 16 * j + 4 * g), acc[i][j]);
+            store4(p, m0 + wm + 16 * i + li, n0 + wn + 16 * j + 4 * g, acc[i][j]);
 }
 
 template <class Cfg, MxType T>
@@ -195,11 +230,134 @@ hipError_t launch_wtile(const MxGemmArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Few rows of A (at most 16 MT): B is streamed once.  A workgroup owns 16 NT
+// rows of B; its waves take units of 128 k in turn (four blocks of each row,
+// one to each lane group), hold a unit's operands and the next one's in
+// registers, and add their parts in LDS at the end, in wave order.
+template <MxType T, int MT, int NT, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW) void mx_wrows_kernel(MxGemmArgs p) {
+    __shared__ mx_f4 part[NW][MT * NT][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int li = lane & 15, g = lane >> 4;
+    const long long n0 = (long long)blockIdx.x * (16 * NT);
+    const long long ks = ((long long)p.K + 31) / 32;
+    const unsigned char *b[NT], *sb[NT], *a[MT];
+    bool has[MT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const long long n = min(n0 + 16 * j + li, (long long)p.N - 1);
+        b[j] = p.B + n * p.ldb;
+        sb[j] = p.SB + n * p.ldsb;
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int m = 16 * i + li;
+        has[i] = m < p.M;
+        a[i] = p.A + (has[i] ? m : 0) * p.lda;
+    }
+    struct Unit {
+        uint4 b[NT], a[MT][4];
+        unsigned s[NT];
+    };
+    auto load = [&](Unit& u, long long k0) {
+        const long long k = k0 + 32 * g;     // the lane's block
+        const bool full = k0 + 128 <= p.K;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if (full) {
+                u.b[j] = mx_load16<VEC>(b[j] + k / 2, 16);
+                u.s[j] = sb[j][k / 32];
+            } else {
+                u.b[j] = mx_codes16<VEC>(b[j], k / 2, p.K);
+                u.s[j] = k / 32 < ks ? sb[j][k / 32] : 127u;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                u.a[i][t] = make_uint4(0u, 0u, 0u, 0u);
+                if (has[i])
+                    u.a[i][t] = load_a<VEC>(a[i] + 2 * k + 16 * t, full ? 16 : 2 * (p.K - k) - 16 * t);
+            }
+    };
+    mx_f4 acc[MT][NT] = {};
+    auto step = [&](const Unit& u, auto split) {
+        float s[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s[j] = mx_scale(u.s[j]);
+        static_for<4>([&](auto t) {
+            uint4 v[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                v[j] = decode8<T, split>(t == 0 ? u.b[j].x : t == 1 ? u.b[j].y : t == 2 ? u.b[j].z : u.b[j].w, s[j]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) mfma_row<T, split, NT>(v, u.a[i][t], acc[i]);
+        });
+    };
+    Unit cur, next;
+    long long k0 = 128ll * wave;
+    if (k0 < p.K) load(cur, k0);
+    while (k0 < p.K) {
+        const long long k1 = k0 + 128 * NW;
+        if (k1 < p.K) load(next, k1);
+        bool in_range = true;
+        if constexpr (T == MxType::f16) {
+            bool ok = true;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) ok = ok && f16_holds(cur.s[j]);
+            in_range = __all(ok);
+        }
+        if (in_range)
+            step(cur, std::false_type{});
+        else
+            step(cur, std::true_type{});
+        cur = next;
+        k0 = k1;
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
+    __syncthreads();
+    for (int t = wave; t < MT * NT; t += NW) {
+        mx_f4 v = part[0][t][lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) v += part[w][t][lane];
+        store4(p, 16 * (t / NT) + li, n0 + 16 * (t % NT) + 4 * g, v);
+    }
+}
+
+template <MxType T, int MT, int NT, int NW>
+hipError_t launch_wrows_cfg(const MxGemmArgs& a, hipStream_t s) {
+    const unsigned grid = (unsigned)(((long long)a.N + 16 * NT - 1) / (16 * NT));
+    if (mx_aligned(a.A, a.lda, 16) && mx_aligned(a.B, a.ldb, 16))
+        mx_wrows_kernel<T, MT, NT, NW, true><<<grid, 64 * NW, 0, s>>>(a);
+    else
+        mx_wrows_kernel<T, MT, NT, NW, false><<<grid, 64 * NW, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <MxType T, int MT>
+hipError_t launch_wrows(const MxGemmArgs& a, hipStream_t s) {
+    constexpr int NT4 = MT == 1 ? 4 : MT == 2 || T == MxType::bf16 ? 2 : 1, NT2 = NT4 < 2 ? NT4 : 2;
+    if ((long long)a.N >= 128ll * a.cus) return launch_wrows_cfg<T, MT, NT4, 8>(a, s);
+    if ((long long)a.N >= 32ll * a.cus && a.M > 1) return launch_wrows_cfg<T, MT, NT2, 8>(a, s);
+    return launch_wrows_cfg<T, MT, 1, 8>(a, s);
+}
+
+template <MxType T>
+hipError_t launch_w(const MxGemmArgs& a, hipStream_t s) {
+    if (a.M <= 16) return launch_wrows<T, 1>(a, s);
+    if (a.M <= 32) return launch_wrows<T, 2>(a, s);
+    if (a.M <= 64) return launch_wrows<T, 4>(a, s);
+    return launch_wtile<WTile<128, 128, 64, 64>, T>(a, s);
+}
+
 }  // namespace
 
 hipError_t launch_mx_wgemm(const MxGemmArgs& a, MxType t, hipStream_t s) {
-    return t == MxType::bf16 ? launch_wtile<WTile<128, 128, 64, 64>, MxType::bf16>(a, s)
-                             : launch_wtile<WTile<128, 128, 64, 64>, MxType::f16>(a, s);
+    return t == MxType::bf16 ? launch_w<MxType::bf16>(a, s) : launch_w<MxType::f16>(a, s);
 }
 
 }  // namespace sgemm
