@@ -18,7 +18,7 @@
 
 namespace sgemm {
 
-enum class MxType { f32, bf16, f16 };
+enum class MxType { f32, bf16, f16, mxfp4 };
 
 // X (R x C) -> Q, S along rows and/or QT, ST along columns (null: not asked).
 struct MxQuantArgs {
@@ -67,6 +67,10 @@ hipError_t launch_mx_gemm(const MxGemmArgs& a, MxType out, hipStream_t s);
 // t: the type of A, bf16 or f16; C is fp32.
 hipError_t launch_mx_wgemm(const MxGemmArgs& a, MxType t, hipStream_t s);
 
+// Both products for at most 64 rows of A, whose type is a_type (mxfp4, bf16 or
+// f16); C's type is out (f32, or bf16 where A is mxfp4).
+hipError_t launch_mx_rows(const MxGemmArgs& a, MxType a_type, MxType out, hipStream_t s);
+
 inline bool mx_aligned(const void* p, long long ld_bytes, int n) {
     return ((unsigned long long)(size_t)p | (unsigned long long)ld_bytes) % n == 0;
 }
@@ -81,22 +85,34 @@ typedef int mx_i8 __attribute__((ext_vector_type(8)));
 // The scale operand of the conversions for a scale byte.
 __device__ __forceinline__ float mx_scale(unsigned byte) { return __uint_as_float(byte << 23); }
 
-// The 16 bytes at p, of which the first n (any sign, at most 16) exist: zeros
-// for the rest, which are not read.  ALIGNED: p is 16-byte aligned.
+// Bytes at .. at + 15 of a row of len: zeros past its end, which is not read.
+// ALIGNED: row + at is 16-byte aligned.  A piece that crosses the row's end is
+// the row's last 16 bytes moved down; a row of less than 16 is read by bytes.
 template <bool ALIGNED>
-__device__ __forceinline__ uint4 mx_load16(const unsigned char* p, long long n) {
+__device__ __forceinline__ uint4 mx_bytes16(const unsigned char* row, long long at, long long len) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    const long long n = len - at;
     if (n >= 16) {
         if constexpr (ALIGNED)
-            v = *reinterpret_cast<const uint4*>(p);
+            v = *reinterpret_cast<const uint4*>(row + at);
         else
-            __builtin_memcpy(&v, p, 16);
+            __builtin_memcpy(&v, row + at, 16);
     } else if (n > 0) {
-        unsigned w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 15; ++i)
-            if (i < n) w[i / 4] |= (unsigned)p[i] << (8 * (i % 4));
-        v = make_uint4(w[0], w[1], w[2], w[3]);
+        unsigned long long lo = 0, hi = 0;
+        if (len >= 16) {
+            unsigned long long w[2];
+            __builtin_memcpy(w, row + len - 16, 16);
+            const int s = 8 * (16 - (int)n);             // 8 .. 120
+            lo = s >= 64 ? w[1] >> (s - 64) : w[0] >> s | w[1] << (64 - s);
+            hi = s >= 64 ? 0ull : w[1] >> s;
+        } else {
+#pragma unroll 1
+            for (int i = (int)n; i-- > 0;) {
+                hi = hi << 8 | lo >> 56;
+                lo = lo << 8 | row[at + i];
+            }
+        }
+        v = make_uint4((unsigned)lo, (unsigned)(lo >> 32), (unsigned)hi, (unsigned)(hi >> 32));
     }
     return v;
 }
@@ -117,8 +133,8 @@ __device__ __forceinline__ uint4 mx_drop_half(uint4 v, long long n) {
 // zeros for elements past K, which are not looked at.
 template <bool ALIGNED>
 __device__ __forceinline__ uint4 mx_codes16(const unsigned char* row, long long at, int K) {
-    const long long left = ((long long)K + 1) / 2 - at;
-    uint4 v = mx_load16<ALIGNED>(row + at, left);
+    const long long len = ((long long)K + 1) / 2, left = len - at;
+    uint4 v = mx_bytes16<ALIGNED>(row, at, len);
     if ((K & 1) && left > 0 && left <= 16) v = mx_drop_half(v, left);
     return v;
 }
@@ -148,21 +164,140 @@ __device__ __forceinline__ uint4 mx_keep(uint4 v, int left) {
     return make_uint4(word(v.x, 0), word(v.y, 1), word(v.z, 2), word(v.w, 3));
 }
 
+#endif
 // The DMA loaders address a tile's rows by 32-bit offsets from its first row.
 inline bool mx_dma_reach(long long ld_bytes, int rows) { return ld_bytes * rows < (1ll << 32); }
-
-// Four registers, each holding in lane group t (of 16 lanes) what groups 0 to
-// 3 need for tile t; afterwards register t holds in lane group g what group g
-// needs for tile t: a transpose across the lane groups.
-__device__ __forceinline__ void mx_transpose4(unsigned (&d)[4]) {
-    const auto a = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
-    const auto x = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-    const auto y = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-    d[0] = x[0];
-    d[1] = x[1];
-    d[2] = y[0];
-    d[3] = y[1];
+// Whether a product takes the few-row kernel: at most 16 rows, or at most 64
+// where 128 x 128 tiles would leave CUs idle (64 rows x 65536 x 8192 takes 87 us
+// in the few-row kernel and 46 in tiles, x 8192 x 8192 18 and 35); and 64 rows
+// of every operand in reach of 32-bit offsets.
+inline bool mx_few_rows(const MxGemmArgs& a) {
+    return (a.M <= 16 || (a.M <= 64 && ((long long)a.N + 127) / 128 < a.cus)) && mx_dma_reach(a.lda, 64) &&
+           mx_dma_reach(a.ldsa, 64) && mx_dma_reach(a.ldb, 64) && mx_dma_reach(a.ldsb, 64);
 }
+#ifdef __HIPCC__
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+
+// acc += the 16 x 16 x 128 product of MXFP4 operands (16 rows of B, of A), with byte SEL of each scale register.
+template <int SEL>
+__device__ __forceinline__ mx_f4 mfma_mx(uint4 b, unsigned sb, uint4 a, unsigned sa, mx_f4 acc) {
+    const mx_i8 bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+    const mx_i8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc, 4, 4, SEL, (int)sb, SEL, (int)sa);
+}
+
+// The eight values of four bytes of codes: in A's type, or (SPLIT) in bfloat16.
+template <MxType T, bool SPLIT>
+__device__ __forceinline__ uint4 decode8(unsigned q, float s) {
+    unsigned v[4];
+    static_for<4>([&](auto i) {
+        if constexpr (T == MxType::bf16 || SPLIT)
+            v[i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, i));
+        else
+            v[i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, i));
+    });
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Two binary16 values as bfloat16 hi and lo with hi + lo their exact sum: hi
+// is the value's upper part (truncated), lo the rest.  An infinity is hi
+// alone; a NaN stays NaN in hi (binary16's payload lies in the upper bits).
+__device__ __forceinline__ void split2(unsigned h2, unsigned& hi, unsigned& lo) {
+    const mx_h2 h = __builtin_bit_cast(mx_h2, h2);
+    const float x = (float)h[0], y = (float)h[1];
+    const unsigned xb = __float_as_uint(x) & 0xFFFF0000u, yb = __float_as_uint(y) & 0xFFFF0000u;
+    const float xh = __uint_as_float(xb), yh = __uint_as_float(yb);
+    const float xl = x == xh ? 0.f : x - xh, yl = y == yh ? 0.f : y - yh;
+    hi = (xb >> 16) | yb;
+    lo = (__float_as_uint(xl) >> 16) | (__float_as_uint(yl) & 0xFFFF0000u);
+}
+
+__device__ __forceinline__ mx_f4 mfma_bf16(uint4 b, uint4 a, mx_f4 acc) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, b), __builtin_bit_cast(bf8, a),
+                                                   acc, 0, 0, 0);
+}
+
+// Whether binary16 holds every value of a block with this scale byte: the
+// smallest, 2^(byte - 128), from its least subnormal 2^-24, the largest,
+// 6 2^(byte - 127), to 65504.
+__device__ __forceinline__ bool f16_holds(unsigned byte) { return byte - 104u <= 36u; }
+
+// acc[j] += a step of 32 k for N tiles of B's rows (decoded by decode8 with
+// the same SPLIT) and one tile of A's.
+template <MxType T, bool SPLIT, int N>
+__device__ __forceinline__ void mfma_row(const uint4 (&b)[N], uint4 a, mx_f4 (&acc)[N]) {
+    if constexpr (T == MxType::bf16) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = mfma_bf16(b[j], a, acc[j]);
+    } else if constexpr (SPLIT) {
+        uint4 hi, lo;
+        split2(a.x, hi.x, lo.x);
+        split2(a.y, hi.y, lo.y);
+        split2(a.z, hi.z, lo.z);
+        split2(a.w, hi.w, lo.w);
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = mfma_bf16(b[j], lo, mfma_bf16(b[j], hi, acc[j]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, b[j]),
+                                                            __builtin_bit_cast(half8, a), acc[j], 0, 0, 0);
+    }
+}
+
+// One row's four neighbouring outputs from column col on.
+template <MxType OUT>
+__device__ __forceinline__ void store4(const MxGemmArgs& p, long long row, long long col, mx_f4 v) {
+    if (row >= p.M || col >= p.N) return;
+    const int n = (int)min(p.N - col, 4ll);
+    if constexpr (OUT == MxType::f32) {
+        float* c = static_cast<float*>(p.C) + row * p.ldc + col;
+        if (n == 4 && ((size_t)c & 15) == 0) {
+            store_c4(c, v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) store_c(c + i, v[i]);
+        }
+    } else {
+        __bf16* c = static_cast<__bf16*>(p.C) + row * p.ldc + col;
+        typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+        if (n == 4 && ((size_t)c & 7) == 0) {
+            *reinterpret_cast<bf4*>(c) = bf4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) c[i] = (__bf16)v[i];
+        }
+    }
+}
+
+// 16 scale bytes of a row of n, from byte `at` on where they exist; else the
+// row's last 16, or its n < 16 and zeros.
+__device__ __forceinline__ void scales16(const unsigned char* row, int at, int n, unsigned (&s)[4]) {
+    __builtin_memcpy(s, row + min(at, n - 16), 16);
+}
+__device__ __forceinline__ void scales_few(const unsigned char* row, int n, unsigned (&s)[4]) {
+    unsigned char v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = row[min(i, n - 1)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i / 4] |= (i < n ? (unsigned)v[i] : 0u) << (8 * (i % 4));
+}
+// 16 bytes moved down by n (0 .. 15, wave-uniform), zeros above.
+__device__ __forceinline__ void down16(unsigned (&s)[4], int n) {
+    for (int k = n >> 2; k > 0; --k) {
+        s[0] = s[1];
+        s[1] = s[2];
+        s[2] = s[3];
+        s[3] = 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = __builtin_amdgcn_alignbyte(i < 3 ? s[i + 1] : 0u, s[i], n & 3);
+}
+
 #endif
 }  // namespace sgemm

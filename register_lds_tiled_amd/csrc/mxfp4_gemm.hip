@@ -16,14 +16,6 @@
 namespace sgemm {
 namespace {
 
-// acc += the 16 x 16 x 128 product, with byte SEL of each scale register.
-template <int SEL>
-__device__ __forceinline__ mx_f4 mfma_mx(uint4 b, unsigned sb, uint4 a, unsigned sa, mx_f4 acc) {
-    const mx_i8 bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-    const mx_i8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc, 4, 4, SEL, (int)sb, SEL, (int)sa);
-}
-
 // The same for 32 x 32 x 64: lane l holds block l / 32 of row l % 32; D as
 // store_tile describes it, its rows the first operand's.  This form runs at
 // the matrix cores' full rate from one wave per SIMD (9.6 PFLOP/s on zeros, 6.7
@@ -35,33 +27,6 @@ __device__ __forceinline__ floatx16 mfma_mx32(uint4 a, unsigned sa, uint4 b, uns
     const mx_i8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
     const mx_i8 bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, acc, 4, 4, SEL, (int)sa, SEL, (int)sb);
-}
-
-// One row's four neighbouring outputs from column col on.
-template <MxType OUT>
-__device__ __forceinline__ void store4(const MxGemmArgs& p, long long row, long long col, mx_f4 v) {
-    if (row >= p.M || col >= p.N) return;
-    const int n = (int)min(p.N - col, 4ll);
-    if constexpr (OUT == MxType::f32) {
-        float* c = static_cast<float*>(p.C) + row * p.ldc + col;
-        if (n == 4 && ((size_t)c & 15) == 0) {
-            store_c4(c, v[0], v[1], v[2], v[3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) store_c(c + i, v[i]);
-        }
-    } else {
-        __bf16* c = static_cast<__bf16*>(p.C) + row * p.ldc + col;
-        typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
-        if (n == 4 && ((size_t)c & 7) == 0) {
-            *reinterpret_cast<bf4*>(c) = bf4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) c[i] = (__bf16)v[i];
-        }
-    }
 }
 
 // Tiles: a workgroup owns BM x BN outputs and walks K in stages of 256 (128
@@ -148,7 +113,7 @@ __global__ __launch_bounds__(Cfg::NT) void mx_tile_kernel(MxGemmArgs p, int tile
     auto fetch = [&](long long k0) {
         if (k0 + Cfg::BK <= p.K) {
 #pragma unroll
-            for (int u = 0; u < CH; ++u) v[u] = mx_load16<false>(src[u] + k0 / 2 + 16 * ((tid + u * NT) & 7), 16);
+            for (int u = 0; u < CH; ++u) __builtin_memcpy(&v[u], src[u] + k0 / 2 + 16 * ((tid + u * NT) & 7), 16);
             __builtin_memcpy(s, ssrc + k0 / 32, 8);
         } else {
 #pragma unroll
@@ -190,32 +155,6 @@ __global__ __launch_bounds__(Cfg::NT) void mx_tile_kernel(MxGemmArgs p, int tile
         });
     }
     store_wave<OUT>(p, acc, m0 + wm, n0 + wn, li, g);
-}
-
-// 16 scale bytes of a row of n, from byte `at` on where they exist; else the
-// row's last 16, or its n < 16 and zeros.
-__device__ __forceinline__ void scales16(const unsigned char* row, int at, int n, unsigned (&s)[4]) {
-    __builtin_memcpy(s, row + min(at, n - 16), 16);
-}
-__device__ __forceinline__ void scales_few(const unsigned char* row, int n, unsigned (&s)[4]) {
-    unsigned char v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = row[min(i, n - 1)];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = 0u;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s[i / 4] |= (i < n ? (unsigned)v[i] : 0u) << (8 * (i % 4));
-}
-// 16 bytes moved down by n (0 .. 15, wave-uniform), zeros above.
-__device__ __forceinline__ void down16(unsigned (&s)[4], int n) {
-    for (int k = n >> 2; k > 0; --k) {
-        s[0] = s[1];
-        s[1] = s[2];
-        s[2] = s[3];
-        s[3] = 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = __builtin_amdgcn_alignbyte(i < 3 ? s[i + 1] : 0u, s[i], n & 3);
 }
 
 // The same tiles where rows lie 16-byte aligned: both operands come by DMA into
@@ -420,127 +359,9 @@ hipError_t launch_tile(const MxGemmArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Few rows of A (at most 16 MT): B is streamed once.  A workgroup owns 16 NT
-// rows of B; its waves take the spans of 512 k in turn, hold a span's operands
-// and the next one's in registers, and add their parts in LDS at the end, in
-// wave order.  Lane group g takes blocks 4g .. 4g + 3 of a span, one in each
-// of four steps: a lane's scales of the span are then four neighbouring bytes,
-// one register for all steps.
-template <int MT, int NT, int NW, MxType OUT, bool VEC>
-__global__ __launch_bounds__(64 * NW) void mx_rows_kernel(MxGemmArgs p) {
-    __shared__ mx_f4 part[NW > 1 ? NW : 1][MT * NT][64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int li = lane & 15, g = lane >> 4;
-    const long long n0 = (long long)blockIdx.x * (16 * NT);
-    const long long ks = ((long long)p.K + 31) / 32;
-    const unsigned char *b[NT], *sb[NT], *a[MT], *sa[MT];
-    bool has[MT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const long long n = min(n0 + 16 * j + li, (long long)p.N - 1);
-        b[j] = p.B + n * p.ldb;
-        sb[j] = p.SB + n * p.ldsb;
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int m = 16 * i + li;
-        has[i] = m < p.M;
-        a[i] = p.A + (has[i] ? m : 0) * p.lda;
-        sa[i] = p.SA + (has[i] ? m : 0) * p.ldsa;
-    }
-    struct Span {
-        uint4 b[NT][4], a[MT][4];
-        unsigned sb[NT], sa[MT];
-    };
-    auto load_row = [&](const unsigned char* q, const unsigned char* s, long long k0, uint4 (&v)[4], unsigned& sc) {
-        const long long at = k0 / 2 + 64 * g;
-        unsigned w[1];
-        if (k0 + 512 <= p.K) {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) v[h] = mx_load16<VEC>(q + at + 16 * h, 16);
-            __builtin_memcpy(w, s + k0 / 32 + 4 * g, 4);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) v[h] = mx_codes16<VEC>(q, at + 16 * h, p.K);
-            mx_scales<4>(s, k0 / 32 + 4 * g, ks, w);
-        }
-        sc = w[0];
-    };
-    auto load = [&](Span& t, long long k0) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) load_row(b[j], sb[j], k0, t.b[j], t.sb[j]);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) t.a[i][h] = make_uint4(0u, 0u, 0u, 0u);
-            t.sa[i] = 0u;
-            if (has[i]) load_row(a[i], sa[i], k0, t.a[i], t.sa[i]);
-        }
-    };
-    mx_f4 acc[MT][NT] = {};
-    Span cur, next;
-    long long k0 = 512ll * wave;
-    if (k0 < p.K) load(cur, k0);
-    while (k0 < p.K) {
-        const long long k1 = k0 + 512 * NW;
-        if (k1 < p.K) load(next, k1);
-        static_for<4>([&](auto h) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    acc[i][j] = mfma_mx<h>(cur.b[j][h], cur.sb[j], cur.a[i][h], cur.sa[i], acc[i][j]);
-        });
-        cur = next;
-        k0 = k1;
-    }
-    if constexpr (NW > 1) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
-        __syncthreads();
-        for (int t = wave; t < MT * NT; t += NW) {
-            mx_f4 v = part[0][t][lane];
-#pragma unroll
-            for (int w = 1; w < NW; ++w) v += part[w][t][lane];
-            store4<OUT>(p, 16 * (t / NT) + li, n0 + 16 * (t % NT) + 4 * g, v);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) store4<OUT>(p, 16 * i + li, n0 + 16 * j + 4 * g, acc[i][j]);
-    }
-}
-
-template <int MT, int NT, int NW, MxType OUT>
-hipError_t launch_rows_cfg(const MxGemmArgs& a, hipStream_t s) {
-    const unsigned grid = (unsigned)(((long long)a.N + 16 * NT - 1) / (16 * NT));
-    if (mx_aligned(a.A, a.lda, 16) && mx_aligned(a.B, a.ldb, 16))
-        mx_rows_kernel<MT, NT, NW, OUT, true><<<grid, 64 * NW, 0, s>>>(a);
-    else
-        mx_rows_kernel<MT, NT, NW, OUT, false><<<grid, 64 * NW, 0, s>>>(a);
-    return hipGetLastError();
-}
-
-template <int MT, MxType OUT>
-hipError_t launch_rows(const MxGemmArgs& a, hipStream_t s) {
-    // Two tiles of B's rows to a workgroup where that leaves two workgroups
-    // for every CU; waves for the spans there are.
-    constexpr int NT = MT < 4 ? 2 : 1;
-    const bool two = (long long)a.N >= 64ll * a.cus;
-    const int spans = (a.K + 511) / 512;
-    if (spans >= 5)
-        return two ? launch_rows_cfg<MT, NT, 8, OUT>(a, s) : launch_rows_cfg<MT, 1, 8, OUT>(a, s);
-    return two ? launch_rows_cfg<MT, NT, 2, OUT>(a, s) : launch_rows_cfg<MT, 1, 2, OUT>(a, s);
-}
-
 template <MxType OUT>
 hipError_t launch_out(const MxGemmArgs& a, hipStream_t s) {
-    if (a.M <= 16) return launch_rows<1, OUT>(a, s);
-    if (a.M <= 32) return launch_rows<2, OUT>(a, s);
-    if (a.M <= 64) return launch_rows<4, OUT>(a, s);
+    if (mx_few_rows(a)) return launch_mx_rows(a, MxType::mxfp4, OUT, s);
     const bool dma = mx_aligned(a.A, a.lda, 16) && mx_aligned(a.B, a.ldb, 16) && a.K > 0 &&
                      mx_dma_reach(a.lda, 256) && mx_dma_reach(a.ldb, 256);
     if (!dma) return launch_tile<MxTile<128, 128, 64, 64>, OUT>(a, s);
