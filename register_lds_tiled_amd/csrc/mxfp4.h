@@ -85,6 +85,15 @@ typedef int mx_i8 __attribute__((ext_vector_type(8)));
 // The scale operand of the conversions for a scale byte.
 __device__ __forceinline__ float mx_scale(unsigned byte) { return __uint_as_float(byte << 23); }
 
+// v moved down by n bytes (1 and up), zeros above.
+__device__ __forceinline__ uint4 mx_down(uint4 v, int n) {
+    const unsigned long long x = v.x | (unsigned long long)v.y << 32, y = v.z | (unsigned long long)v.w << 32;
+    const int s = 8 * n;
+    unsigned long long lo = s >= 64 ? y >> (s & 63) : x >> s | y << (64 - s), hi = s >= 64 ? 0ull : y >> s;
+    if (s >= 128) lo = 0ull;
+    return make_uint4((unsigned)lo, (unsigned)(lo >> 32), (unsigned)hi, (unsigned)(hi >> 32));
+}
+
 // Bytes at .. at + 15 of a row of len: zeros past its end, which is not read.
 // ALIGNED: row + at is 16-byte aligned.  A piece that crosses the row's end is
 // the row's last 16 bytes moved down; a row of less than 16 is read by bytes.
@@ -100,11 +109,8 @@ __device__ __forceinline__ uint4 mx_bytes16(const unsigned char* row, long long 
     } else if (n > 0) {
         unsigned long long lo = 0, hi = 0;
         if (len >= 16) {
-            unsigned long long w[2];
-            __builtin_memcpy(w, row + len - 16, 16);
-            const int s = 8 * (16 - (int)n);             // 8 .. 120
-            lo = s >= 64 ? w[1] >> (s - 64) : w[0] >> s | w[1] << (64 - s);
-            hi = s >= 64 ? 0ull : w[1] >> s;
+            __builtin_memcpy(&v, row + len - 16, 16);
+            return mx_down(v, 16 - (int)n);
         } else {
 #pragma unroll 1
             for (int i = (int)n; i-- > 0;) {

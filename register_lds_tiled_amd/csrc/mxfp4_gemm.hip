@@ -76,6 +76,39 @@ __device__ __forceinline__ void store_wave(const MxGemmArgs& p, const floatx16 (
     }
 }
 
+// mfma_mx32 in place on accumulation registers, as an instruction of its own:
+// from the builtin the compiler copies 16-register accumulators about and
+// spills in the widest tile (64 per lane and 1000 and more bytes of scratch at
+// 128 x 128 outputs a wave).  It knows nothing of the wait states the
+// instruction needs: two after a vector instruction writes an operand, and 19
+// before its result is read (mfma_settled, mfma_done).
+template <int SEL>
+__device__ __forceinline__ void mfma_mx32_in(floatx16& acc, uint4 a, unsigned sa, uint4 b, unsigned sb) {
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 av = {a.x, a.y, a.z, a.w}, bv = {b.x, b.y, b.z, b.w};
+    if constexpr (SEL == 0)
+        asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : "+a"(acc) : "v"(av), "v"(bv), "v"(sa), "v"(sb));
+    else if constexpr (SEL == 1)
+        asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] "
+                     "cbsz:4 blgp:4" : "+a"(acc) : "v"(av), "v"(bv), "v"(sa), "v"(sb));
+    else if constexpr (SEL == 2)
+        asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[1,1,0] cbsz:4 blgp:4"
+                     : "+a"(acc) : "v"(av), "v"(bv), "v"(sa), "v"(sb));
+    else
+        asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0] "
+                     "cbsz:4 blgp:4" : "+a"(acc) : "v"(av), "v"(bv), "v"(sa), "v"(sb));
+}
+__device__ __forceinline__ void mfma_settled() { asm volatile("s_nop 3" ::: "memory"); }
+template <int FM, int FN>
+__device__ __forceinline__ void mfma_done(floatx16 (&acc)[FM][FN]) {
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) asm volatile("" : "+a"(acc[i][j]));   // reads stay behind the pause
+}
+
 // The register-staged form, for rows of any alignment and pitch.
 template <class Cfg, MxType OUT>
 __global__ __launch_bounds__(Cfg::NT) void mx_tile_kernel(MxGemmArgs p, int tiles_m, int tiles_n) {
@@ -161,10 +194,11 @@ __global__ __launch_bounds__(Cfg::NT) void mx_tile_kernel(MxGemmArgs p, int tile
 // one of two LDS stages, the next stage requested right after the barrier that
 // ends the reads of its place and waited for a stage's multiplication later.
 //
-// Scales come straight to registers, 16 bytes (512 k, two stages) of 64 rows
-// by one load: lane 32 t + r holds row r of tile t, in words w0 .. w3.  Lane
-// half g needs words g (first stage) and 2 + g (second) of both tiles: one
-// exchange of lane halves per stage brings them there.
+// Scales of 2048 k (64 bytes of every row) lie in LDS beside the stages, chunk c
+// of row r at c ^ (r / 4 & 3).  They are read along the rows while the last
+// stage that needs the ones before multiplies, and written after it.  (Loaded
+// straight to the lanes that need them, a row a lane, they took the address
+// unit as long as half the codes: 8192^3 to bf16 369 us, 307 without.)
 //
 // Past K: a chunk that begins past a row's end is read from the row's last
 // one, and what is past K in A's last stage is cleared in LDS; B's codes
@@ -175,9 +209,11 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::OCC) void mx_dma_kernel(MxGemmArgs p,
     constexpr int BM = Cfg::BM, BN = Cfg::BN, NW = Cfg::NW, FM = Cfg::FM, FN = Cfg::FN;
     constexpr int IA = BM * 8 / 64 / NW, IB = BN * 8 / 64 / NW;   // a wave's DMA instructions per stage
     static_assert(IA * NW * 64 == BM * 8 && IB * NW * 64 == BN * 8, "whole DMA rounds");
-    static_assert(FM % 2 == 0 && FN % 2 == 0, "64 rows of scales at a time");
+    constexpr int IS = (BM + BN) * 4 / Cfg::NT;                   // a thread's 16-byte pieces of scales
+    static_assert(IS * Cfg::NT == (BM + BN) * 4, "whole rounds of scales");
     constexpr unsigned STAGE = (BM + BN) * 128;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
+    __shared__ __attribute__((aligned(16))) uint4 sc[(BM + BN) * 4];   // A's rows, then B's
     int tm, tn;
     tile_coords(blockIdx.x, tiles_m, tiles_n, Cfg::GROUP_M, p.xcds, tm, tn);
     const int tid = threadIdx.x, lane = tid & 63;
@@ -204,7 +240,7 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::OCC) void mx_dma_kernel(MxGemmArgs p,
     for (int u = 0; u < IB; ++u)
         vb[u] = (unsigned)min((wave + u * NW) * 8 + (lane >> 3), nlast) * (unsigned)p.ldb;
     const unsigned lds0 = lds_addr(lds);
-    auto request = [&](int s) {
+    auto request = [&](int s) __attribute__((always_inline)) {
         const unsigned at = (unsigned)min(c, chunks - 1 - 8 * s) * 16u;
         const unsigned to = lds0 + (s & 1) * STAGE + 1024u * wave;
         const unsigned char* const a = A + 128ll * s;
@@ -216,45 +252,54 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::OCC) void mx_dma_kernel(MxGemmArgs p,
         for (int u = 0; u < IB; ++u)
             lds_dma16s(b, vb[u] + at, __builtin_amdgcn_readfirstlane(to + BM * 128 + u * NW * 1024u));
     };
-    const unsigned char* sa[FM / 2];
-    const unsigned char* sb[FN / 2];
-#pragma unroll
-    for (int i = 0; i < FM / 2; ++i) sa[i] = p.SA + (m0 + min(wm + 64 * i + lane, mlast)) * p.ldsa;
-#pragma unroll
-    for (int j = 0; j < FN / 2; ++j) sb[j] = p.SB + (n0 + min(wn + 64 * j + lane, nlast)) * p.ldsb;
-    unsigned ra[FM / 2][4], rb[FN / 2][4];       // as loaded for the next pair of stages
-    unsigned fa[2][FM], fb[2][FN];               // by stage of the pair, a register a tile
-    auto load_scales = [&](int s) {
-#pragma unroll
-        for (int i = 0; i < FM / 2; ++i) scales16(sa[i], 8 * s, chunks, ra[i]);
-#pragma unroll
-        for (int j = 0; j < FN / 2; ++j) scales16(sb[j], 8 * s, chunks, rb[j]);
+    // A row's bytes from 64 panel on; past its end its last 16 instead, moved
+    // down when they are placed.
+    uint4 piece[IS];
+    static_assert(BM * 4 % Cfg::NT == 0, "a round of scales is A's or B's");
+    auto scale_row = [&](auto u) __attribute__((always_inline)) {
+        constexpr int r0 = u * Cfg::NT / 4;
+        const int r = r0 + (tid >> 2);
+        if constexpr (r0 < BM)
+            return p.SA + (m0 + min(r, mlast)) * p.ldsa;
+        else
+            return p.SB + (n0 + min(r - BM, nlast)) * p.ldsb;
     };
-    auto place_scales = [&] {
-        static_for<2>([&](auto q) {
-#pragma unroll
-            for (int i = 0; i < FM / 2; ++i) {
-                const auto x = __builtin_amdgcn_permlane32_swap(ra[i][2 * q], ra[i][2 * q + 1], false, false);
-                fa[q][2 * i] = x[0];
-                fa[q][2 * i + 1] = x[1];
-            }
-#pragma unroll
-            for (int j = 0; j < FN / 2; ++j) {
-                const auto x = __builtin_amdgcn_permlane32_swap(rb[j][2 * q], rb[j][2 * q + 1], false, false);
-                fb[q][2 * j] = x[0];
-                fb[q][2 * j + 1] = x[1];
-            }
+    const int sat = 16 * (tid & 3);
+    auto load_scales = [&](int panel) __attribute__((always_inline)) {
+        const int at = min(64 * panel + sat, chunks - 16);
+        static_for<IS>([&](auto u) { __builtin_memcpy(&piece[u], scale_row(u) + at, 16); });
+    };
+    auto place_scales = [&](int panel) __attribute__((always_inline)) {
+        const int past = chunks < 16 ? 0 : max(64 * panel + sat - (chunks - 16), 0);
+        static_for<IS>([&](auto u) {
+            const int r = (tid + u * Cfg::NT) >> 2;
+            uint4* const to = &sc[r * 4 + ((tid ^ (r >> 2)) & 3)];
+            lds_poison_f4(to);
+            *to = past == 0 ? piece[u] : mx_down(piece[u], past);
         });
+    };
+    unsigned fa[2][FM], fb[2][FN];               // by stage of a pair, a register a tile
+    auto read_scales = [&](int s) __attribute__((always_inline)) {
+        const int c = s >> 1;                    // the pair's chunk, mod 4
+        auto read = [&](int r, unsigned& even, unsigned& odd) {
+            const unsigned* const w = reinterpret_cast<const unsigned*>(&sc[r * 4 + ((c ^ (r >> 2)) & 3)]) + g;
+            even = w[0];
+            odd = w[2];
+        };
+#pragma unroll
+        for (int i = 0; i < FM; ++i) read(wm + 32 * i + li, fa[0][i], fa[1][i]);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) read(BM + wn + 32 * j + li, fb[0][j], fb[1][j]);
     };
 
     floatx16 acc[FM][FN] = {};
     // One stage: in step h, lane half g has block 8 s + 4 g + h.
-    auto multiply = [&](auto odd) {
+    auto multiply = [&](auto odd) __attribute__((always_inline)) {
         const unsigned char* const st = lds + (odd ? STAGE : 0u);
         // a step's operands are read while the step before multiplies; the
         // barriers keep the compiler from reading the whole stage at once
         uint4 a[2][FM], b[2][FN];
-        auto read = [&](auto h) {
+        auto read = [&](auto h) __attribute__((always_inline)) {
             const int at = ((4 * g + h) ^ place_of(li)) * 16;
 #pragma unroll
             for (int j = 0; j < FN; ++j)
@@ -264,27 +309,28 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::OCC) void mx_dma_kernel(MxGemmArgs p,
                 a[h & 1][i] = *reinterpret_cast<const uint4*>(st + (wm + 32 * i + li) * 128 + at);
         };
         read(std::integral_constant<int, 0>{});
+        mfma_settled();
         static_for<4>([&](auto h) {
             if constexpr (h < 3) read(std::integral_constant<int, h + 1>{});
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
-                    acc[i][j] = mfma_mx32<h>(a[h & 1][i], fa[odd][i], b[h & 1][j], fb[odd][j], acc[i][j]);
+                    mfma_mx32_in<h>(acc[i][j], a[h & 1][i], fa[odd][i], b[h & 1][j], fb[odd][j]);
             __builtin_amdgcn_sched_barrier(0);
         });
     };
     // The requested stage is there, for all waves, and the other one's reads
     // are over.
-    auto arrived = [&] {
+    auto arrived = [&]() __attribute__((always_inline)) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
     };
-    // A's elements past K, in the last stage, become 0.
-    auto clear_past = [&](int s) {
-        if ((p.K & 255) == 0) return;
+    // A's elements past K in a stage become 0.
+    auto clear_past = [&](int s) __attribute__((always_inline)) {
+        if (256ll * (s + 1) <= p.K) return;
         for (int id = tid; id < BM * 8; id += Cfg::NT) {
-            const int left = p.K - 32 * (8 * s + ((id & 7) ^ place_of(id >> 3)));
+            const int left = (int)(p.K - 32ll * (8 * s + ((id & 7) ^ place_of(id >> 3))));
             uint4* const v = reinterpret_cast<uint4*>(lds + (s & 1) * STAGE + 16 * id);
             if (left < 32) *v = mx_keep(*v, left);
         }
@@ -292,45 +338,34 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::OCC) void mx_dma_kernel(MxGemmArgs p,
     };
     constexpr std::integral_constant<int, 0> even{};
     constexpr std::integral_constant<int, 1> odd{};
-    if (chunks >= 16) {
+    if (chunks >= 16)
         load_scales(0);
-    } else {
-#pragma unroll
-        for (int i = 0; i < FM / 2; ++i) scales_few(sa[i], chunks, ra[i]);
-#pragma unroll
-        for (int j = 0; j < FN / 2; ++j) scales_few(sb[j], chunks, rb[j]);
-    }
+    else
+        static_for<IS>([&](auto u) __attribute__((always_inline)) {
+            piece[u] = mx_bytes16<false>(scale_row(u), sat, chunks);
+        });
     request(0);
-    // Pairs of stages that another follows, then the last pair or single stage.
+    place_scales(0);
+    // Pairs of stages.  One copy of the multiplication, in the loop: from a
+    // second one after it the compiler copies the accumulators, without the
+    // wait states that takes.  So where K ends in a pair's first stage, the
+    // second multiplies zeros.
     int s = 0;
-    for (; s + 2 < stages; s += 2) {
+    do {                                         // K > 0
         arrived();
-        place_scales();
-        load_scales(s + 2);
-        request(s + 1);
-        multiply(even);
-        arrived();
-        request(s + 2);
-        multiply(odd);
-    }
-    arrived();
-    if (const int past = 8 * s + 16 - chunks; past > 0 && chunks >= 16) {
-#pragma unroll
-        for (int i = 0; i < FM / 2; ++i) down16(ra[i], past);
-#pragma unroll
-        for (int j = 0; j < FN / 2; ++j) down16(rb[j], past);
-    }
-    place_scales();
-    if (s + 1 < stages) {
-        request(s + 1);
-        multiply(even);
-        arrived();
-        clear_past(s + 1);
-        multiply(odd);
-    } else {
+        read_scales(s);
         clear_past(s);
+        if (s + 1 < stages) request(s + 1);
         multiply(even);
-    }
+        arrived();
+        const bool turn = (s & 7) == 6 && s + 2 < stages;   // the panel's last scales have been read
+        if (turn) load_scales((s + 2) >> 3);
+        clear_past(s + 1);
+        if (s + 2 < stages) request(s + 2);
+        multiply(odd);
+        if (turn) place_scales((s + 2) >> 3);
+    } while ((s += 2) < stages);
+    mfma_done(acc);
     store_wave<OUT>(p, acc, m0 + wm, n0 + wn, li, g);
 }
 
@@ -365,9 +400,15 @@ hipError_t launch_out(const MxGemmArgs& a, hipStream_t s) {
     const bool dma = mx_aligned(a.A, a.lda, 16) && mx_aligned(a.B, a.ldb, 16) && a.K > 0 &&
                      mx_dma_reach(a.lda, 256) && mx_dma_reach(a.ldb, 256);
     if (!dma) return launch_tile<MxTile<128, 128, 64, 64>, OUT>(a, s);
-#ifdef MXT_
-    return launch_dma<MxTile<MXT_>, OUT>(a, s);
-#endif
+    // Rounds of workgroups, one 256 x 256 or two 128 x 128 to a CU, times what a
+    // round takes (8192^3: 71 us of four rounds, 43 of eight).  The wide tiles
+    // read half as much through L2, whose rate bounds the others: 8192^3 297
+    // against 330 us, 4096 x 8192 x 4096 83 against 100; 2048^3, 64 wide tiles,
+    // 20 against 11.
+    const long long wide = ((long long)a.M + 255) / 256 * (((long long)a.N + 255) / 256);
+    const long long small = ((long long)a.M + 127) / 128 * (((long long)a.N + 127) / 128);
+    if (5 * ((wide + a.cus - 1) / a.cus) <= 3 * ((small + 2 * a.cus - 1) / (2 * a.cus)))
+        return launch_dma<MxTile<256, 256, 128, 64, 2>, OUT>(a, s);
     return launch_dma<MxTile<128, 128, 64, 64, 2>, OUT>(a, s);
 }
 
