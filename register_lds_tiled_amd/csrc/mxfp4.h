@@ -33,7 +33,7 @@ struct MxQuantArgs {
     long long ldqt;
     unsigned char* ST;
     long long ldst;
-    int xcds = 8;
+    int cus = 256, xcds = 8;
 };
 struct MxDequantArgs {
     int R, C;

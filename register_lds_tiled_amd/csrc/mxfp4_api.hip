@@ -63,8 +63,7 @@ int quantize(int R, int C, const void* X, int ldx, void* Q, int ldq, void* S, in
                   static_cast<unsigned char*>(Q), ldq, static_cast<unsigned char*>(S), lds,
                   static_cast<unsigned char*>(QT), ldqt, static_cast<unsigned char*>(ST), ldst};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    int cus;
-    hipError_t e = device_shape(s, cus, a.xcds);
+    hipError_t e = device_shape(s, a.cus, a.xcds);
     if (e != hipSuccess) return hip_fail(e);
     e = launch_mx_quantize(a, t, s);
     return e == hipSuccess ? SGEMM_OK : hip_fail(e);

@@ -73,11 +73,13 @@ __global__ __launch_bounds__(Cfg::NT, 1) void mx_wtile_kernel(MxGemmArgs p, int 
 #pragma unroll
         for (int u = 0; u < CA; ++u) {
             const int id = tid + u * NT, r = id >> 4, c = id & 15;
+            lds_poison_f4(&as[r * 16 + (c ^ (r & 15))]);
             as[r * 16 + (c ^ (r & 15))] = va[u];
         }
 #pragma unroll
         for (int u = 0; u < CB; ++u) {
             const int id = tid + u * NT, r = id >> 2, c = id & 3;
+            lds_poison_f4(&bs[r * 4 + (c ^ ((r >> 1) & 3))]);
             bs[r * 4 + (c ^ ((r >> 1) & 3))] = vb[u];
         }
         if (tid < BN) sc[tid] = s[0];
@@ -270,9 +272,8 @@ __global__ __launch_bounds__(Cfg::NT, 2) void mx_wdma_kernel(MxGemmArgs p, int t
         if ((p.K & 127) == 0) return;
         unsigned char* const st = lds + (s & 1) * STAGE;
         for (int id = tid; id < BM * 16; id += Cfg::NT) {
-            const int left = p.K - 128 * s - 8 * (((id & 15) ^ (id >> 4)) & 15);
+            const int left = (int)(p.K - 128ll * s) - 8 * (((id & 15) ^ (id >> 4)) & 15);
             uint4* const v = reinterpret_cast<uint4*>(st + 16 * id);
-            // eight 16-bit elements: as 16 halves of a byte of codes, twice
             if (left < 8) {
                 const uint4 k = *v;
                 auto word = [&](unsigned w, int i) {
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(Cfg::NT, 2) void mx_wdma_kernel(MxGemmArgs p, int t
             }
         }
         for (int id = tid; id < BN * 4; id += Cfg::NT) {
-            const int left = p.K - 128 * s - 32 * (((id & 3) ^ (id >> 4)) & 3);
+            const int left = (int)(p.K - 128ll * s) - 32 * (((id & 3) ^ (id >> 4)) & 3);
             uint4* const v = reinterpret_cast<uint4*>(st + BM * 256 + 16 * id);
             if (left < 32) *v = mx_keep(*v, left);
         }
