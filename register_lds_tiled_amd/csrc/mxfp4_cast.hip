@@ -44,6 +44,13 @@ __device__ __forceinline__ unsigned quad_max(unsigned v) {
     return with_lane_xor<2>(with_lane_xor<1>(v, max_of), max_of);
 }
 
+// N bytes from an address of any alignment: the memory unit takes wide accesses
+// at every byte address.
+template <int N>
+__device__ __forceinline__ void unaligned_copy(void* to, const void* from) {
+    __builtin_memcpy(reinterpret_cast<unsigned char*>(to), reinterpret_cast<const unsigned char*>(from), N);
+}
+
 // Eight consecutive elements in a lane's registers, by type: loads (guarded:
 // the first n elements exist, the others are 0), the magnitudes' maximum as
 // float bits, and conversion of pairs.
@@ -54,13 +61,10 @@ template <>
 struct Eight<MxType::f32> {
     static constexpr int SIZE = 4;
     unsigned w[8];
-    template <bool VEC>
     __device__ __forceinline__ void load(const void* base, long long at, int n) {
         const unsigned* p = static_cast<const unsigned*>(base) + at;
-        if (VEC && n >= 8) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 4);
-            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-            w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+        if (n >= 8) {
+            unaligned_copy<32>(w, p);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = i < n ? p[i] : 0u;
@@ -111,12 +115,10 @@ template <MxType T>
 struct Eight {
     static constexpr int SIZE = 2;
     unsigned w[4];
-    template <bool VEC>
     __device__ __forceinline__ void load(const void* base, long long at, int n) {
         const unsigned short* p = static_cast<const unsigned short*>(base) + at;
-        if (VEC && n >= 8) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p);
-            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        if (n >= 8) {
+            unaligned_copy<16>(w, p);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -179,10 +181,9 @@ __device__ __forceinline__ unsigned scale_byte(unsigned bits) {
 }
 
 // Store of the first n (1 .. 4) bytes of q.
-template <bool VEC>
 __device__ __forceinline__ void store_bytes(unsigned char* p, unsigned q, int n) {
-    if (VEC && n >= 4) {
-        *reinterpret_cast<unsigned*>(p) = q;
+    if (n >= 4) {
+        __builtin_memcpy(p, &q, 4);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -218,7 +219,7 @@ Items items_of(int R, int C, int E, int at_a_time) {
 // are short, several rows' (lpr: log2 of lanes per row).  Items (segments of
 // row groups) are numbered along the rows; a wave takes four neighbours at a
 // time and loads them all before it converts the first.
-template <MxType T, bool VEC>
+template <MxType T>
 __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(MxQuantArgs p, int lpr, unsigned segs,
                                                                long long items) {
     const int lane = threadIdx.x & 63;
@@ -242,7 +243,7 @@ __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(MxQuantArgs p, in
             const long long c = ((long long)seg << lpr) * 8 + unit * 8;
             const bool in = first + u < items && row[u] < p.R && c < p.C;
             col[u] = in ? (int)c : -1;
-            x[u].template load<VEC>(p.X, in ? row[u] * p.ldx + c : 0, in ? min(p.C - (int)c, 8) : 0);
+            x[u].load(p.X, in ? row[u] * p.ldx + c : 0, in ? min(p.C - (int)c, 8) : 0);
         }
 #pragma unroll
         for (int u = 0; u < kCastItems; ++u) {
@@ -250,7 +251,7 @@ __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(MxQuantArgs p, in
             const unsigned byte = scale_byte(Eight<T>::top_bits(m));
             const unsigned q = x[u].codes(mx_scale(byte));
             if (col[u] < 0) continue;
-            store_bytes<VEC>(p.Q + row[u] * p.ldq + col[u] / 2, q, (min(p.C - col[u], 8) + 1) / 2);
+            store_bytes(p.Q + row[u] * p.ldq + col[u] / 2, q, (min(p.C - col[u], 8) + 1) / 2);
             if ((lane & 3) == 0) p.S[row[u] * p.lds + col[u] / 32] = (unsigned char)byte;
         }
     }
@@ -260,17 +261,19 @@ __global__ __launch_bounds__(256) void mx_quantize_rows_kernel(MxQuantArgs p, in
 // workgroup owns a piece of kTileR x 128; each wave takes 32 rows of it (one
 // block of every column), 64 columns at a time: lane l holds rows 4 (l / 8) .. + 3,
 // columns 8 (l % 8) .. + 7.  A row's blocks are quads of lanes; a column's
-// block is the lanes of equal l % 8.  The transposed codes, 2 bytes per lane
-// and column, and scales are gathered in LDS and leave as whole segments down
-// the columns.
+// block is the lanes of equal l % 8.  Codes and scales are gathered in LDS and
+// leave as whole segments of rows and columns.
 constexpr int kTileC = 128;
 
-template <MxType T, bool VEC, bool ROWS, int kTileR>
+template <MxType T, bool ROWS, int kTileR>
 __global__ __launch_bounds__(2 * kTileR) void mx_quantize_both_kernel(MxQuantArgs p, int tiles_m, int tiles_n) {
-    constexpr int kTileWaves = kTileR / 32;
+    constexpr int kTileWaves = kTileR / 32, NT = 64 * kTileWaves;
     constexpr int kTilePitch = kTileR / 2 + 4;   // LDS bytes of a column's codes: odd in words
+    constexpr int kRowPitch = kTileC / 2 + 4;    // of a row's
     __shared__ __attribute__((aligned(16))) unsigned char qt[kTileC * kTilePitch];
     __shared__ __attribute__((aligned(16))) unsigned char st[kTileC * kTileWaves];
+    __shared__ __attribute__((aligned(16))) unsigned char qr[ROWS ? kTileR * kRowPitch : 4];
+    __shared__ __attribute__((aligned(16))) unsigned char sr[ROWS ? kTileR * (kTileC / 32) : 4];
     int tm, tn;
     tile_coords(blockIdx.x, tiles_m, tiles_n, 8, p.xcds, tm, tn);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -286,7 +289,7 @@ __global__ __launch_bounds__(2 * kTileR) void mx_quantize_both_kernel(MxQuantArg
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bool in = r + i < p.R && n > 0;
-            x[i].template load<VEC>(p.X, in ? (r + i) * p.ldx + c : 0, in ? n : 0);
+            x[i].load(p.X, in ? (r + i) * p.ldx + c : 0, in ? n : 0);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) cols.take(x[i]);
@@ -296,10 +299,9 @@ __global__ __launch_bounds__(2 * kTileR) void mx_quantize_both_kernel(MxQuantArg
                 const unsigned m = quad_max(x[i].top());
                 const unsigned byte = scale_byte(Eight<T>::top_bits(m));
                 const unsigned q = x[i].codes(mx_scale(byte));
-                if (r + i < p.R && n > 0) {
-                    store_bytes<VEC>(p.Q + (r + i) * p.ldq + c / 2, q, (n + 1) / 2);
-                    if ((lane & 3) == 0) p.S[(r + i) * p.lds + c / 32] = (unsigned char)byte;
-                }
+                const int row = wave * 32 + rg * 4 + i;
+                *reinterpret_cast<unsigned*>(&qr[row * kRowPitch + half * 32 + cg * 4]) = q;
+                if ((lane & 3) == 0) sr[row * (kTileC / 32) + half * 2 + (cg >> 2)] = (unsigned char)byte;
             }
         }
         cols.template across<8>();
@@ -315,49 +317,62 @@ __global__ __launch_bounds__(2 * kTileR) void mx_quantize_both_kernel(MxQuantArg
         }
     }
     __syncthreads();
-    // Bytes and scales of this tile that exist down a column.
+    // A run of codes (16-byte pieces, PER of them to a line of `pitch` bytes in
+    // LDS) or scales (PER bytes a line) of the lines that exist.
+    auto store_codes = [&](const unsigned char* from, int pitch, auto PER, int lines, int n, unsigned char* to,
+                           long long ld) {
+        for (int id = threadIdx.x; id < lines * PER; id += NT) {
+            const int line = id / PER, at = id % PER * 16;
+            const unsigned* w = reinterpret_cast<const unsigned*>(from + line * pitch + at);
+            unsigned char* out = to + line * ld + at;
+            if (at + 16 <= n) {
+                const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+                __builtin_memcpy(out, &v, 16);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (at + 4 * j < n) store_bytes(out + 4 * j, w[j], min(n - at - 4 * j, 4));
+            }
+        }
+    };
+    auto store_scales = [&](const unsigned char* from, auto PER, int lines, int n, unsigned char* to, long long ld) {
+        for (int line = threadIdx.x; line < lines; line += NT) {
+            unsigned char* out = to + line * ld;
+            const unsigned char* in = from + line * PER;
+            if (n == PER) {
+                __builtin_memcpy(out, in, PER);      // any alignment
+            } else {
+                for (int i = 0; i < n; ++i) out[i] = in[i];
+            }
+        }
+    };
     const int rows = (int)min((long long)p.R - r0, (long long)kTileR);
-    const int nbytes = (rows + 1) / 2, nscales = (rows + 31) / 32;
-    constexpr int PER = kTileR / 32;             // 16-byte chunks down a column
-    constexpr int NT = 64 * kTileWaves;
-#pragma unroll
-    for (int k = 0; k < kTileC * PER / NT; ++k) {
-        const int id = threadIdx.x + NT * k, col = id / PER, at = id % PER * 16;
-        if (c0 + col >= p.C) continue;
-        const unsigned* w = reinterpret_cast<const unsigned*>(&qt[col * kTilePitch + at]);
-        unsigned char* out = p.QT + (c0 + col) * p.ldqt + r0 / 2 + at;
-        if (VEC && at + 16 <= nbytes) {
-            *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (at + 4 * j < nbytes) store_bytes<VEC>(out + 4 * j, w[j], min(nbytes - at - 4 * j, 4));
-        }
-    }
-    for (int col = threadIdx.x; col < kTileC && c0 + col < p.C; col += NT) {
-        unsigned char* out = p.ST + (c0 + col) * p.ldst + r0 / 32;
-        const unsigned char* in = &st[col * kTileWaves];
-        if (nscales == kTileWaves) {
-            __builtin_memcpy(out, in, kTileWaves);   // any alignment
-        } else {
-            for (int i = 0; i < nscales; ++i) out[i] = in[i];
-        }
+    const int ncols = (int)min((long long)p.C - c0, (long long)kTileC);
+    store_codes(qt, kTilePitch, std::integral_constant<int, kTileR / 32>{}, ncols, (rows + 1) / 2,
+                p.QT + c0 * p.ldqt + r0 / 2, p.ldqt);
+    store_scales(st, std::integral_constant<int, kTileWaves>{}, ncols, (rows + 31) / 32, p.ST + c0 * p.ldst + r0 / 32,
+                 p.ldst);
+    if constexpr (ROWS) {
+        store_codes(qr, kRowPitch, std::integral_constant<int, kTileC / 32>{}, rows, (ncols + 1) / 2,
+                    p.Q + r0 * p.ldq + c0 / 2, p.ldq);
+        store_scales(sr, std::integral_constant<int, kTileC / 32>{}, rows, (ncols + 31) / 32,
+                     p.S + r0 * p.lds + c0 / 32, p.lds);
     }
 }
 
-template <MxType T, bool VEC, int ROWS>
+template <MxType T, int ROWS>
 hipError_t launch_both(const MxQuantArgs& a, long long tn, hipStream_t s) {
     const long long tm = ((long long)a.R + ROWS - 1) / ROWS;
     constexpr int NT = 2 * ROWS;
     if (tm * tn * NT > 0xFFFFFFFFll) return hipErrorInvalidValue;
     if (a.Q != nullptr)
-        mx_quantize_both_kernel<T, VEC, true, ROWS><<<(unsigned)(tm * tn), NT, 0, s>>>(a, (int)tm, (int)tn);
+        mx_quantize_both_kernel<T, true, ROWS><<<(unsigned)(tm * tn), NT, 0, s>>>(a, (int)tm, (int)tn);
     else
-        mx_quantize_both_kernel<T, VEC, false, ROWS><<<(unsigned)(tm * tn), NT, 0, s>>>(a, (int)tm, (int)tn);
+        mx_quantize_both_kernel<T, false, ROWS><<<(unsigned)(tm * tn), NT, 0, s>>>(a, (int)tm, (int)tn);
     return hipGetLastError();
 }
 
-template <MxType T, bool VEC>
+template <MxType T>
 hipError_t quantize_t(const MxQuantArgs& a, hipStream_t s) {
     if (a.QT != nullptr) {
         // 256 rows at a time where that leaves two workgroups to a CU (lines of
@@ -365,24 +380,17 @@ hipError_t quantize_t(const MxQuantArgs& a, hipStream_t s) {
         // against 95), else 128 (1000 x 777 12.7 against 15.9).
         const long long tn = ((long long)a.C + kTileC - 1) / kTileC;
         const bool tall = ((long long)a.R + 255) / 256 * tn >= 2 * a.cus;
-        return tall ? launch_both<T, VEC, 256>(a, tn, s) : launch_both<T, VEC, 128>(a, tn, s);
+        return tall ? launch_both<T, 256>(a, tn, s) : launch_both<T, 128>(a, tn, s);
     }
     const Items it = items_of(a.R, a.C, 8, kCastItems);
-    mx_quantize_rows_kernel<T, VEC><<<it.grid, 256, 0, s>>>(a, it.lpr, it.segs, it.items);
+    mx_quantize_rows_kernel<T><<<it.grid, 256, 0, s>>>(a, it.lpr, it.segs, it.items);
     return hipGetLastError();
-}
-
-template <MxType T>
-hipError_t quantize_v(const MxQuantArgs& a, hipStream_t s) {
-    constexpr int e = Eight<T>::SIZE;
-    const bool vec = mx_aligned(a.X, a.ldx * e, 16) && (a.Q == nullptr || mx_aligned(a.Q, a.ldq, 4)) &&
-                     (a.QT == nullptr || mx_aligned(a.QT, a.ldqt, 16));
-    return vec ? quantize_t<T, true>(a, s) : quantize_t<T, false>(a, s);
 }
 
 // Reading back: a lane takes 16 bytes of output -- 4 floats or 8 16-bit values
 // -- so that a wave's stores are whole kilobytes; lanes and items as in the
 // row quantiser.
+// VEC: rows of Y start 16-byte aligned.
 template <MxType T, bool VEC>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(MxDequantArgs p, int lpr, unsigned segs,
                                                             long long items) {
@@ -411,9 +419,8 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(MxDequantArgs p, int
             byte[u] = 0u;
             if (!in) continue;
             const unsigned char* src = p.Q + row[u] * p.ldq + c / 2;
-            if (VEC && p.C - c >= E) {
-                if constexpr (E == 8) q[u] = *reinterpret_cast<const unsigned*>(src);
-                else q[u] = *reinterpret_cast<const unsigned short*>(src);
+            if (p.C - c >= E) {
+                __builtin_memcpy(&q[u], src, E / 2);
             } else {
                 const int n = (min(p.C - (int)c, E) + 1) / 2;
 #pragma unroll
@@ -438,6 +445,8 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(MxDequantArgs p, int
                 unsigned* y = static_cast<unsigned*>(p.Y) + at;
                 if (VEC && n == E) {
                     __builtin_nontemporal_store(u32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<u32x4*>(y));
+                } else if (n == E) {
+                    unaligned_copy<16>(y, v);
                 } else {
 #pragma unroll
                     for (int i = 0; i < E; ++i)
@@ -453,9 +462,11 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(MxDequantArgs p, int
                     h[i] = T == MxType::bf16 ? v[i] >> 16
                                              : __builtin_bit_cast(unsigned short, (_Float16)__uint_as_float(v[i]));
                 unsigned short* y = static_cast<unsigned short*>(p.Y) + at;
+                const u32x4 o = {h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
                 if (VEC && n == E) {
-                    __builtin_nontemporal_store(u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
-                                                      h[6] | h[7] << 16}, reinterpret_cast<u32x4*>(y));
+                    __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(y));
+                } else if (n == E) {
+                    unaligned_copy<16>(y, &o);
                 } else {
 #pragma unroll
                     for (int i = 0; i < E; ++i)
@@ -470,7 +481,7 @@ template <MxType T>
 hipError_t dequantize_v(const MxDequantArgs& a, hipStream_t s) {
     constexpr int E = T == MxType::f32 ? 4 : 8, ITEMS = 32 / E;
     const Items it = items_of(a.R, a.C, E, ITEMS);
-    const bool vec = mx_aligned(a.Q, a.ldq, E / 2) && mx_aligned(a.Y, a.ldy * Eight<T>::SIZE, 16);
+    const bool vec = mx_aligned(a.Y, a.ldy * Eight<T>::SIZE, 16);
     if (vec)
         mx_dequantize_kernel<T, true><<<it.grid, 256, 0, s>>>(a, it.lpr, it.segs, it.items);
     else
@@ -482,9 +493,9 @@ hipError_t dequantize_v(const MxDequantArgs& a, hipStream_t s) {
 
 hipError_t launch_mx_quantize(const MxQuantArgs& a, MxType t, hipStream_t s) {
     switch (t) {
-        case MxType::f32: return quantize_v<MxType::f32>(a, s);
-        case MxType::bf16: return quantize_v<MxType::bf16>(a, s);
-        default: return quantize_v<MxType::f16>(a, s);
+        case MxType::f32: return quantize_t<MxType::f32>(a, s);
+        case MxType::bf16: return quantize_t<MxType::bf16>(a, s);
+        default: return quantize_t<MxType::f16>(a, s);
     }
 }
 
