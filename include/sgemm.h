@@ -235,8 +235,9 @@ SGEMM_API int gemm_f16_f32(int M, int N, int K,
  * for a leading dimension below a row's bytes, SGEMM_EALIAS also for an output
  * that overlaps an input or another output; extents run from a matrix's first
  * byte to its last row's end, so scales may not lie between the rows of the
- * values they belong to).  Bytes outside the R rows and their row lengths are
- * neither read nor written.  Nothing is allocated, no workspace is used, and
+ * values they belong to).  What lies past a row's length is never written and
+ * never matters; an input row on 16-byte boundaries may be read to the end of
+ * its last 16 bytes.  Nothing is allocated, no workspace is used, and
  * every result is the same from call to call.
  */
 

@@ -94,18 +94,14 @@ __device__ __forceinline__ uint4 mx_down(uint4 v, int n) {
     return make_uint4((unsigned)lo, (unsigned)(lo >> 32), (unsigned)hi, (unsigned)(hi >> 32));
 }
 
-// Bytes at .. at + 15 of a row of len: zeros past its end, which is not read.
-// ALIGNED: row + at is 16-byte aligned.  A piece that crosses the row's end is
-// the row's last 16 bytes moved down; a row of less than 16 is read by bytes.
-template <bool ALIGNED>
+// Bytes at .. at + 15 of a row of len, of any alignment: zeros past its end,
+// which is not read.  A piece that crosses the row's end is the row's last 16
+// bytes moved down; a row of less than 16 is read by bytes.
 __device__ __forceinline__ uint4 mx_bytes16(const unsigned char* row, long long at, long long len) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     const long long n = len - at;
     if (n >= 16) {
-        if constexpr (ALIGNED)
-            v = *reinterpret_cast<const uint4*>(row + at);
-        else
-            __builtin_memcpy(&v, row + at, 16);
+        __builtin_memcpy(&v, row + at, 16);
     } else if (n > 0) {
         unsigned long long lo = 0, hi = 0;
         if (len >= 16) {
@@ -137,15 +133,14 @@ __device__ __forceinline__ uint4 mx_drop_half(uint4 v, long long n) {
 
 // 16 bytes of codes at byte `at` of a row of K codes that starts at `row`:
 // zeros for elements past K, which are not looked at.
-template <bool ALIGNED>
 __device__ __forceinline__ uint4 mx_codes16(const unsigned char* row, long long at, int K) {
     const long long len = ((long long)K + 1) / 2, left = len - at;
-    uint4 v = mx_bytes16<ALIGNED>(row, at, len);
+    uint4 v = mx_bytes16(row, at, len);
     if ((K & 1) && left > 0 && left <= 16) v = mx_drop_half(v, left);
     return v;
 }
 
-// N (4, 8 or 16) scale bytes from byte `at` of a row of n: zeros past n.
+// N (4 or 8) scale bytes from byte `at` of a row of n: zeros past n.
 template <int N>
 __device__ __forceinline__ void mx_scales(const unsigned char* row, long long at, long long n,
                                           unsigned (&s)[N / 4]) {
@@ -174,18 +169,26 @@ __device__ __forceinline__ uint4 mx_keep(uint4 v, int left) {
 // The DMA loaders address a tile's rows by 32-bit offsets from its first row.
 inline bool mx_dma_reach(long long ld_bytes, int rows) { return ld_bytes * rows < (1ll << 32); }
 // Whether a product takes the few-row kernel: at most 16 rows, or at most 64
-// where 128 x 128 tiles would leave CUs idle (64 rows x 65536 x 8192 takes 87 us
-// in the few-row kernel and 46 in tiles, x 8192 x 8192 18 and 35); and 64 rows
-// of every operand in reach of 32-bit offsets.
+// where 128 x 128 tiles would leave half the CUs idle (64 rows, K = 8192: N =
+// 8192 takes 18 us in the few-row kernel and 34 in tiles, 24576 54 and 39; with
+// 16-bit A 34 and 62, 100 and 66); and 64 rows of every operand in reach of
+// 32-bit offsets.
 inline bool mx_few_rows(const MxGemmArgs& a) {
-    return (a.M <= 16 || (a.M <= 64 && ((long long)a.N + 127) / 128 < a.cus)) && mx_dma_reach(a.lda, 64) &&
+    return (a.M <= 16 || (a.M <= 64 && 2 * (((long long)a.N + 127) / 128) < a.cus)) && mx_dma_reach(a.lda, 64) &&
            mx_dma_reach(a.ldsa, 64) && mx_dma_reach(a.ldb, 64) && mx_dma_reach(a.ldsb, 64);
 }
 #ifdef __HIPCC__
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 
-// acc += the 16 x 16 x 128 product of MXFP4 operands (16 rows of B, of A), with byte SEL of each scale register.
+// v_mfma_scale_f32_16x16x128_f8f6f4 on 4-bit elements: lane l holds 32
+// consecutive elements (16 bytes, one block) of row l % 16 of each operand, and
+// their scale in byte SEL of one register.  The order of the k terms is free, so
+// which blocks the four lane groups l / 16 take together is chosen for the
+// memory side.  D: lane l, register i is row 4 (l / 16) + i of the first operand,
+// row l % 16 of the second; B's rows go first, so a lane holds four neighbouring
+// columns of one row of C.  (Layout, scale bytes 0 and 255 and the accuracy
+// checked on the GPU: within 2.5e-8 sum |a b| of the exact sum of 128 terms.)
 template <int SEL>
 __device__ __forceinline__ mx_f4 mfma_mx(uint4 b, unsigned sb, uint4 a, unsigned sa, mx_f4 acc) {
     const mx_i8 bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
@@ -219,6 +222,8 @@ __device__ __forceinline__ void split2(unsigned h2, unsigned& hi, unsigned& lo) 
     lo = (__float_as_uint(xl) >> 16) | (__float_as_uint(yl) & 0xFFFF0000u);
 }
 
+// v_mfma_f32_16x16x32_{bf16,f16}: lane l holds 8 consecutive k of row l % 16 of
+// each operand; D as above.
 __device__ __forceinline__ mx_f4 mfma_bf16(uint4 b, uint4 a, mx_f4 acc) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, b), __builtin_bit_cast(bf8, a),
                                                    acc, 0, 0, 0);

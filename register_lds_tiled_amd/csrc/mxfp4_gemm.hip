@@ -1,24 +1,20 @@
 // mxfp4_gemm.hip -- C = A.B^T with both operands in MXFP4, on the matrix
 // cores, accumulated in fp32.
 //
-// v_mfma_scale_f32_16x16x128_f8f6f4 multiplies a 16 x 128 by a 128 x 16 piece
-// of 4-bit elements: lane l holds 32 consecutive elements (16 bytes, one MX
-// block) of row l % 16 of each operand, and a scale byte for them in a byte,
-// chosen by the instruction, of one register.  The order of the k terms is
-// free, so which blocks the four lane groups l / 16 take together is chosen
-// for the memory side.  D: lane l, register i is row 4 (l / 16) + i of the
-// first operand, row l % 16 of the second.  B's rows are passed first, so a
-// lane holds four neighbouring columns of one row of C.  (Layout, scale bytes
-// 0 and 255 and the sums' accuracy checked on the GPU: within 2.5e-8 of
-// sum |a b| of the exact sum over 128 terms.)
+// At most 64 rows of A: mxfp4_rows.hip.  Else tiles: 256 x 256 and 128 x 128 by
+// DMA, 128 x 128 through registers where rows are not 16-byte aligned.  8192^3
+// takes 273 us to fp32 C and 263 to bfloat16 (4.0 and 4.2 PFLOP/s); the matrix
+// instructions alone would need 164 on random codes, where power limits them,
+// and 112 on zeros.
 #include "mxfp4.h"
 
 namespace sgemm {
 namespace {
 
-// The same for 32 x 32 x 64: lane l holds block l / 32 of row l % 32; D as
-// store_tile describes it, its rows the first operand's.  This form runs at
-// the matrix cores' full rate from one wave per SIMD (9.6 PFLOP/s on zeros, 6.7
+// v_mfma_scale_f32_32x32x64_f8f6f4 on 4-bit elements: lane l holds block l / 32
+// of row l % 32 of each operand, its scale in byte SEL of one register; D as
+// store_tile describes it, its rows the first operand's.  This form runs at the
+// matrix cores' full rate from one wave per SIMD (9.6 PFLOP/s on zeros, 6.7
 // on random codes, which power limits), where 16 x 16 x 128 reaches 5.3 from
 // one wave and 6.9 from two (4.9 and 5.9 on random codes): the tile kernels
 // use it.
@@ -151,7 +147,7 @@ __global__ __launch_bounds__(Cfg::NT) void mx_tile_kernel(MxGemmArgs p, int tile
         } else {
 #pragma unroll
             for (int u = 0; u < CH; ++u)
-                v[u] = mx_codes16<false>(src[u], k0 / 2 + 16 * ((tid + u * NT) & 7), p.K);
+                v[u] = mx_codes16(src[u], k0 / 2 + 16 * ((tid + u * NT) & 7), p.K);
             mx_scales<8>(ssrc, k0 / 32, ks, s);
         }
     };
@@ -342,7 +338,7 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::OCC) void mx_dma_kernel(MxGemmArgs p,
         load_scales(0);
     else
         static_for<IS>([&](auto u) __attribute__((always_inline)) {
-            piece[u] = mx_bytes16<false>(scale_row(u), sat, chunks);
+            piece[u] = mx_bytes16(scale_row(u), sat, chunks);
         });
     request(0);
     place_scales(0);
@@ -402,9 +398,9 @@ hipError_t launch_out(const MxGemmArgs& a, hipStream_t s) {
     if (!dma) return launch_tile<MxTile<128, 128, 64, 64>, OUT>(a, s);
     // Rounds of workgroups, one 256 x 256 or two 128 x 128 to a CU, times what a
     // round takes (8192^3: 71 us of four rounds, 43 of eight).  The wide tiles
-    // read half as much through L2, whose rate bounds the others: 8192^3 297
-    // against 330 us, 4096 x 8192 x 4096 83 against 100; 2048^3, 64 wide tiles,
-    // 20 against 11.
+    // read half as much through L2, whose rate (25 TB/s and more) bounds the
+    // others: 8192^3 297 against 330 us, 4096 x 8192 x 4096 83 against 100;
+    // 2048^3, 64 wide tiles, 20 against 11.
     const long long wide = ((long long)a.M + 255) / 256 * (((long long)a.N + 255) / 256);
     const long long small = ((long long)a.M + 127) / 128 * (((long long)a.N + 127) / 128);
     if (5 * ((wide + a.cus - 1) / a.cus) <= 3 * ((small + 2 * a.cus - 1) / (2 * a.cus)))

@@ -18,7 +18,7 @@
 // is read along its rows and turned in a piece of LDS of the wave's own,
 // without barriers.  (Turning B through LDS too, in stages that the workgroup
 // shares, keeps too little in flight: one token x 8192 x 8192 12 to 17 us
-// against 9.6.)
+// against 9.6.)  Where B has many rows and A is 16-bit, several waves share A.
 //
 // A's piece: 16 MT rows of 16 chunks of 16 bytes; MXFP4: a span, chunk 4g + s
 // for step s; 16-bit: a step, chunk 4g + t with the step's t-th eight elements
@@ -38,19 +38,24 @@ __device__ __forceinline__ void wave_order() {
     __builtin_amdgcn_wave_barrier();
 }
 
-template <MxType A, MxType OUT, int MT, int NT, int NW>
+// SHARED: the waves, four of them, take columns of their own and walk k
+// together; each brings the piece of A of one of a span's four steps, two spans
+// in LDS in turn.
+template <MxType A, MxType OUT, int MT, int NT, int NW, bool SHARED>
 __global__ __launch_bounds__(64 * NW, MT * NT == 1 ? 4 : NW == 8 ? 2 : 1) void mx_rows_kernel(MxGemmArgs p) {
     constexpr bool MX = A == MxType::mxfp4;
+    static_assert(!SHARED || (NW == 4 && !MX), "a wave to each of a span's steps");
     constexpr int PIECE = 16 * MT * 16;                  // chunks of a wave's piece of A
     constexpr int PART = MT * NT * 64;                   // and of its results
     constexpr int MINE = PIECE > PART ? PIECE : PART;
-    __shared__ __attribute__((aligned(16))) uint4 lds[NW * MINE];
+    __shared__ __attribute__((aligned(16))) uint4 lds[SHARED ? 2 * NW * PIECE : NW * MINE];
     __shared__ __attribute__((aligned(16))) uint4 lds_sa[MX ? NW * 16 * MT : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, g = lane >> 4;
-    uint4* const as = lds + wave * MINE;
+    uint4* as = lds + wave * (SHARED ? PIECE : MINE);
     uint4* const ss = lds_sa + (MX ? wave * 16 * MT : 0);
-    const long long n0 = (long long)blockIdx.x * (16 * NT);
+    const long long first = ((long long)blockIdx.x * (SHARED ? NW : 1) + (SHARED ? wave : 0)) * (16 * NT);
+    const long long n0 = SHARED ? min(first, (long long)p.N - 1) : first;
     const long long ks = ((long long)p.K + 31) / 32;
     const int nlast = (int)min((long long)p.N - 1 - n0, 16ll * NT - 1);   // rows past B's last read it again
     // Addresses: a wave-uniform base and a 32-bit offset of the lane's own.
@@ -97,7 +102,7 @@ __global__ __launch_bounds__(64 * NW, MT * NT == 1 ? 4 : NW == 8 ? 2 : 1) void m
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
             for (int h = 0; h < 4; ++h)
-                t.b[j][h] = mx_codes16<false>(B + (ob[j] - 64 * g), k0 / 2 + 64 * g + 16 * h, p.K);
+                t.b[j][h] = mx_codes16(B + (ob[j] - 64 * g), k0 / 2 + 64 * g + 16 * h, p.K);
             unsigned w[1];
             mx_scales<4>(SB + (os[j] - 4 * g), k0 / 32 + 4 * g, ks, w);
             t.s[j] = w[0];
@@ -109,12 +114,12 @@ __global__ __launch_bounds__(64 * NW, MT * NT == 1 ? 4 : NW == 8 ? 2 : 1) void m
             if (4 * u + g < p.M) {
                 const unsigned char* const row = p.A + 4 * u * p.lda + (unsigned)g * (unsigned)p.lda;
                 if constexpr (MX)
-                    t.a[u] = mx_codes16<false>(row, k0 / 2 + chunk, p.K);
+                    t.a[u] = mx_codes16(row, k0 / 2 + chunk, p.K);
                 else
-                    t.a[u] = mx_bytes16<false>(row, 2 * k0 + 64 * s + chunk, 2ll * p.K);
+                    t.a[u] = mx_bytes16(row, 2 * k0 + 64 * s + chunk, 2ll * p.K);
             }
         if constexpr (MX)
-            if (lane < p.M) t.s = mx_bytes16<false>(p.SA + (unsigned)lane * (unsigned)p.ldsa, k0 / 32, ks);
+            if (lane < p.M) t.s = mx_bytes16(p.SA + (unsigned)lane * (unsigned)p.ldsa, k0 / 32, ks);
     };
     auto place_a = [&](const Piece& t) __attribute__((always_inline)) {
         wave_order();
@@ -174,6 +179,47 @@ __global__ __launch_bounds__(64 * NW, MT * NT == 1 ? 4 : NW == 8 ? 2 : 1) void m
             steps(std::true_type{});
     };
     const int spans = p.K / 512;      // whole ones
+    if constexpr (SHARED) {
+        const int all = (int)(((long long)p.K + 511) / 512);
+        Span cur, next;
+        Piece a;
+        // The span's pieces are there for all waves once the last barrier is
+        // passed; the next span's go to the other half meanwhile.
+        auto fetch = [&](Span& t, int i) __attribute__((always_inline)) {
+            if (i < spans) {
+                load_b(t, 512ll * i);
+                load_a(a, 512ll * i, wave);
+            } else {
+                load_b_end(t, 512ll * i);
+                load_a_end(a, 512ll * i, wave);
+            }
+        };
+        auto half = [&](int i) { return lds + (i & 1) * (NW * PIECE); };
+        if (all > 0) {
+            fetch(cur, 0);
+            as = half(0) + wave * PIECE;
+            place_a(a);
+        }
+        __syncthreads();
+        for (int i = 0; i < all; ++i) {
+            if (i + 1 < all) fetch(next, i + 1);
+            static_for<4>([&](auto h) {
+                as = half(i) + h * PIECE;
+                multiply_16(cur, h);
+            });
+            if (i + 1 < all) {
+                as = half(i + 1) + wave * PIECE;
+                place_a(a);
+            }
+            cur = next;
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) store4<OUT>(p, 16 * i + li, first + 16 * j + 4 * g, acc[i][j]);
+        return;
+    }
     Span cur, next;
     Piece a;
     if (wave < spans) {
@@ -230,24 +276,31 @@ __global__ __launch_bounds__(64 * NW, MT * NT == 1 ? 4 : NW == 8 ? 2 : 1) void m
     }
 }
 
-template <MxType A, MxType OUT, int MT, int NT, int NW>
+template <MxType A, MxType OUT, int MT, int NT, int NW, bool SHARED = false>
 hipError_t launch_cfg(const MxGemmArgs& a, hipStream_t s) {
-    const unsigned grid = (unsigned)(((long long)a.N + 16 * NT - 1) / (16 * NT));
-    mx_rows_kernel<A, OUT, MT, NT, NW><<<grid, 64 * NW, 0, s>>>(a);
+    constexpr int columns = 16 * NT * (SHARED ? NW : 1);
+    const unsigned grid = (unsigned)(((long long)a.N + columns - 1) / columns);
+    mx_rows_kernel<A, OUT, MT, NT, NW, SHARED><<<grid, 64 * NW, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <MxType A, MxType OUT, int MT>
 hipError_t launch_mt(const MxGemmArgs& a, hipStream_t s) {
     // More columns to a workgroup read A less often, fewer leave more
-    // workgroups: us at N = 65536 and 8192, K = 8192 (1024 of 1024 with one
-    // column tile and eight waves 2.7, with two 3.0):
-    //                         one token       16 rows       16-bit A, 1 and 16
-    //   16 columns, 8 waves   59.8  10.3     78.1  11.9     70.9  12.0   121  17.8
-    //   32 columns, 8 waves   59.7  10.3     74.8  11.7     73.1  12.5   108  16.0
-    //   64 columns, 4 waves   56.3  15.1     63.8  17.3     67.6  19.7    99  24.5
-    // (binary16's two forms leave no registers for 64: 119 against 100 us.)
-    if (a.N >= 128 * a.cus) return launch_cfg<A, OUT, MT, MT == 4 || A == MxType::f16 ? 2 : 4, 4>(a, s);
+    // workgroups.  us at K = 8192, N = 65536 and 8192:
+    //                            MXFP4 A: one row   16 rows   16-bit A: one row   16 rows
+    //   16 columns, 8 waves         59.8  10.3   78.1  11.9       70.9  12.0    121  17.8
+    //   32 columns, 8 waves         59.7  10.3   74.8  11.7       73.1  12.5    108  16.0
+    //   64 columns, 4 waves         56.3  15.1   63.8  17.3       67.6  19.7     99  24.5
+    //   4 x 32 columns, A shared                                  75.6           82
+    // (At N = K = 1024 16 columns take 2.7, 32 take 3.0.)
+    if (a.N >= 128 * a.cus) {
+        if constexpr (A == MxType::mxfp4)
+            return launch_cfg<A, OUT, MT, MT == 4 ? 2 : 4, 4>(a, s);
+        else
+            return a.M == 1 ? launch_cfg<A, OUT, MT, 2, 4>(a, s)
+                            : launch_cfg<A, OUT, MT, MT == 4 ? 1 : 2, 4, true>(a, s);
+    }
     if (a.N >= 32 * a.cus && a.M > 1) return launch_cfg<A, OUT, MT, MT == 4 && A == MxType::f16 ? 1 : 2, 8>(a, s);
     return launch_cfg<A, OUT, MT, 1, 8>(a, s);
 }
