@@ -4,7 +4,9 @@
  *
  * Operation (every entry point below computes this, the 4x4 case of it, or,
  * for sgemm_f32_ex, this followed by a fused epilogue; gemm_bf16_f32 and
- * gemm_f16_f32 take A and B in 16-bit formats):
+ * gemm_f16_f32 take A and B in 16-bit formats; the MXFP4 entry points, whose
+ * operands are 4-bit elements in scaled blocks and whose B is stored by its
+ * columns, are described where they begin):
  *
  *     C[i,j] = sum_{k=0}^{K-1} A[i,k] * B[k,j]      0 <= i < M, 0 <= j < N
  *

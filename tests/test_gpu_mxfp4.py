@@ -293,6 +293,28 @@ def test_product_wide_tiles_and_long_rows(out, shape):
     check_product(run_product(out, M, N, K, a, sa, bq, sb), A, B, out, 64, what=f"{out} {shape}")
 
 
+# few rows against many columns: each form of the few-row kernel, with whole
+# spans of 512, with an end and with the end alone
+WIDE = [(1, 32770, 1030), (16, 33000, 2100), (5, 40001, 300), (3, 8200, 2600), (16, 8192, 4608), (30, 8200, 700),
+        (60, 9000, 1300)]
+
+
+@pytest.mark.parametrize("shape", WIDE, ids=lambda s: "x".join(map(str, s)))
+def test_few_rows_many_columns(shape):
+    M, N, K = shape
+    rng = np.random.default_rng(M + 5 * N + 7 * K)
+    n = (K + 1) // 2
+    for off in (0, 1):
+        bq, sb, B = operand(rng, N, K, pad=(-n) % 16 + off, spad=off, off=off)
+        a, sa, A = operand(rng, M, K, pad=(-n) % 16 + off, spad=off, off=off)
+        check_product(run_product("f32", M, N, K, a, sa, bq, sb), A, B, "f32", 64, what=f"{shape} offset {off}")
+        for t in ("bf16", "f16"):
+            x, X = a16(rng, M, K, t, pad=(-K) % 8 + off, off=off)
+            C = run_wproduct(t, M, N, K, x, K + (-K) % 8 + off, bq, sb)
+            check_product(C, X, B, "f32", 16, 2, what=f"{t} {shape} offset {off}")
+            assert np.array_equal(C, run_wproduct(t, M, N, K, x, K + (-K) % 8 + off, bq, sb)), "a repeat differs"
+
+
 @pytest.mark.parametrize("t", ["bf16", "f16"])
 @pytest.mark.parametrize("shape", LONG + [(300, 260, 1664)], ids=lambda s: "x".join(map(str, s)))
 def test_weight_product_long_rows(t, shape):

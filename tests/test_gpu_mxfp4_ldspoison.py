@@ -26,7 +26,7 @@ def operand(rng, rows, K, ld):
 
 # few rows (one span, several, an odd end), 128 x 128 tiles by DMA (stages odd
 # and even, past 2048) and register-staged (odd pitch), 256 x 256 tiles
-SHAPES = [(1, 300, 512), (5, 96, 4096), (17, 64, 3001), (64, 130, 2600), (130, 250, 777), (200, 300, 2304),
+SHAPES = [(5, 33000, 1100), (20, 8200, 700), (1, 300, 512), (5, 96, 4096), (17, 64, 3001), (64, 130, 2600), (130, 250, 777), (200, 300, 2304),
           (128, 256, 4401), (4100, 2300, 300), (4096, 2304, 2336)]
 
 
