@@ -263,24 +263,67 @@ __device__ __forceinline__ void store4(const MxGemmArgs& p, long long row, long 
     if (row >= p.M || col >= p.N) return;
     const int n = (int)min(p.N - col, 4ll);
     if constexpr (OUT == MxType::f32) {
+        // (streamed where rows are whole lines: see mx_store_wave)
         float* c = static_cast<float*>(p.C) + row * p.ldc + col;
-        if (n == 4 && ((size_t)c & 15) == 0) {
-            store_c4(c, v[0], v[1], v[2], v[3]);
+        if (n == 4) {
+            if (((unsigned long long)(size_t)p.C | (unsigned long long)p.ldc * 4) % 128 == 0)
+                store_c4(c, v[0], v[1], v[2], v[3]);
+            else
+                __builtin_memcpy(c, &v, 16);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i < n) store_c(c + i, v[i]);
+                if (i < n) c[i] = v[i];
         }
     } else {
         __bf16* c = static_cast<__bf16*>(p.C) + row * p.ldc + col;
         typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
-        if (n == 4 && ((size_t)c & 7) == 0) {
-            *reinterpret_cast<bf4*>(c) = bf4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        if (n == 4) {
+            const bf4 o = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+            __builtin_memcpy(c, &o, 8);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i < n) c[i] = (__bf16)v[i];
         }
+    }
+}
+
+// A wave's outputs from 32 x 32 accumulators, the first of them (r0, c0).  fp32
+// rows on whole lines stream past the caches (8192^3 283 us against 300); others
+// do not, as their pieces of a line meet only there (6336 x 4669 x 90 44 us
+// against 62).
+template <MxType OUT, int FM, int FN>
+__device__ __forceinline__ void mx_store_wave(const MxGemmArgs& p, const floatx16 (&acc)[FM][FN], long long r0,
+                                              long long c0, int li, int g) {
+    typedef std::conditional_t<OUT == MxType::f32, float, __bf16> T;
+    const int rows = (int)min(p.M - r0, 32ll * FM) - 4 * g, cols = (int)min(p.N - c0, 32ll * FN) - li;
+    T* c = static_cast<T*>(p.C) + (r0 + 4 * g) * p.ldc + c0 + li;
+    auto store = [&](auto stream) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = 32 * i + 8 * (r / 4) + r % 4;
+                T* const at = c + row * p.ldc;
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    if (row < rows && 32 * j < cols) {
+                        if constexpr (stream)
+                            __builtin_nontemporal_store((T)acc[i][j][r], at + 32 * j);
+                        else
+                            at[32 * j] = (T)acc[i][j][r];
+                    }
+            }
+        }
+    };
+    if constexpr (OUT == MxType::f32) {
+        if (((unsigned long long)(size_t)p.C | (unsigned long long)p.ldc * 4) % 128 == 0)
+            store(std::true_type{});
+        else
+            store(std::false_type{});
+    } else {
+        store(std::false_type{});
     }
 }
 

@@ -48,31 +48,6 @@ struct MxTile {
     static constexpr int FM = WM / 32, FN = WN / 32;
 };
 
-// A wave's outputs, whose first is (r0, c0).
-template <MxType OUT, int FM, int FN>
-__device__ __forceinline__ void store_wave(const MxGemmArgs& p, const floatx16 (&acc)[FM][FN], long long r0,
-                                           long long c0, int li, int g) {
-    typedef std::conditional_t<OUT == MxType::f32, float, __bf16> T;
-    const int rows = (int)min(p.M - r0, 32ll * FM) - 4 * g, cols = (int)min(p.N - c0, 32ll * FN) - li;
-    T* c = static_cast<T*>(p.C) + (r0 + 4 * g) * p.ldc + c0 + li;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int row = 32 * i + 8 * (r / 4) + r % 4;
-            T* const at = c + row * p.ldc;
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                if (row < rows && 32 * j < cols) {
-                    if constexpr (OUT == MxType::f32)
-                        store_c(at + 32 * j, acc[i][j][r]);
-                    else
-                        at[32 * j] = (__bf16)acc[i][j][r];
-                }
-        }
-    }
-}
-
 // mfma_mx32 in place on accumulation registers, as an instruction of its own:
 // from the builtin the compiler copies 16-register accumulators about and
 // spills in the widest tile (64 per lane and 1000 and more bytes of scratch at
@@ -184,7 +159,7 @@ __global__ __launch_bounds__(Cfg::NT) void mx_tile_kernel(MxGemmArgs p, int tile
                 for (int j = 0; j < FN; ++j) acc[i][j] = mfma_mx32<h>(a[i], sa[i], b[j], sb[j], acc[i][j]);
         });
     }
-    store_wave<OUT>(p, acc, m0 + wm, n0 + wn, li, g);
+    mx_store_wave<OUT>(p, acc, m0 + wm, n0 + wn, li, g);
 }
 
 // The same tiles where rows lie 16-byte aligned: both operands come by DMA into
@@ -363,7 +338,7 @@ __global__ __launch_bounds__(Cfg::NT, Cfg::OCC) void mx_dma_kernel(MxGemmArgs p,
         if (turn) place_scales((s + 2) >> 3);
     } while ((s += 2) < stages);
     mfma_done(acc);
-    store_wave<OUT>(p, acc, m0 + wm, n0 + wn, li, g);
+    mx_store_wave<OUT>(p, acc, m0 + wm, n0 + wn, li, g);
 }
 
 template <class Cfg>

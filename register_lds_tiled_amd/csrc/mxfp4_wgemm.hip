@@ -325,19 +325,7 @@ __global__ __launch_bounds__(Cfg::NT, 2) void mx_wdma_kernel(MxGemmArgs p, int t
             now[j][2] = now[j][3];
         }
     }
-    const int rows = (int)min(p.M - (m0 + wm), (long long)Cfg::WM) - 4 * g;
-    const int cols = (int)min(p.N - (n0 + wn), (long long)Cfg::WN) - li;
-    float* const c = static_cast<float*>(p.C) + (m0 + wm + 4 * g) * p.ldc + n0 + wn + li;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int row = 32 * i + 8 * (r / 4) + r % 4;
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                if (row < rows && 32 * j < cols) store_c(c + row * p.ldc + 32 * j, acc[i][j][r]);
-        }
-    }
+    mx_store_wave<MxType::f32>(p, acc, m0 + wm, n0 + wn, li, g);
 }
 
 template <class Cfg, MxType T>
