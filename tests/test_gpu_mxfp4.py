@@ -410,6 +410,19 @@ def test_weight_product_scale_extremes(t, M):
 
 
 @pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [1, 20, 140])
+def test_weight_product_subnormal_activations(t, M):
+    """A's values below its type's normal range (2^-14, 2^-126) count as they are."""
+    N, K = 150, 416
+    rng = np.random.default_rng(M)
+    lo, hi, size = {"f16": (110, 130, 2.0 ** -17), "bf16": (137, 147, 2.0 ** -129)}[t]
+    a, A = a16(rng, M, K, t, scale_=size)
+    assert (np.abs(A[A != 0]) < {"f16": 2.0 ** -14, "bf16": 2.0 ** -126}[t]).mean() > 0.3
+    bq, sb, B = operand(rng, N, K, lo, hi)
+    check_product(run_wproduct(t, M, N, K, a, K, bq, sb), A, B, "f32", 16, 2, what=f"{t} subnormal A")
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
 @pytest.mark.parametrize("M", [2, 20, 140])
 def test_weight_product_nan_and_infinity(t, M):
     N, K = 150, 416
