@@ -102,7 +102,9 @@ int product(int M, int N, int K, const void* A, int lda, const void* SA, int lds
     if (C == nullptr) return SGEMM_EINVAL_PTR;
     if (K > 0 && (A == nullptr || B == nullptr || SB == nullptr || (mx_a && SA == nullptr)))
         return SGEMM_EINVAL_PTR;
-    // One workgroup per 64 x 64 tile at most: the grid's threads fit a launch.
+    // 256 threads per 64 x 64 tile fit a launch.  No kernel is launched with
+    // more: the few-row forms that take more per column are chosen for narrow
+    // C, or where their grid fits (mxfp4_rows.hip).
     const long long tiles = ((long long)M + 63) / 64 * (((long long)N + 63) / 64);
     if (tiles * 256 > 0xFFFFFFFFll) return SGEMM_EINVAL_DIM;
     Ranges g;

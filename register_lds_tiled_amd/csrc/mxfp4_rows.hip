@@ -294,12 +294,15 @@ hipError_t launch_mt(const MxGemmArgs& a, hipStream_t s) {
     //   64 columns, 4 waves         56.3  15.1   63.8  17.3       67.6  19.7     99  24.5
     //   4 x 32 columns, A shared                                  75.6           82
     // (At N = K = 1024 16 columns take 2.7, 32 take 3.0.)
+    // One row of 16-bit A takes 256 threads to 32 columns while a launch holds
+    // them (N to 2^29 - 32), past that the shared form's 128 (K = 8192, N =
+    // 65536: 70 us and 81).
     if (a.N >= 128 * a.cus) {
         if constexpr (A == MxType::mxfp4)
             return launch_cfg<A, OUT, MT, MT == 4 ? 2 : 4, 4>(a, s);
         else
-            return a.M == 1 ? launch_cfg<A, OUT, MT, 2, 4>(a, s)
-                            : launch_cfg<A, OUT, MT, MT == 4 ? 1 : 2, 4, true>(a, s);
+            return a.M == 1 && a.N <= (1 << 29) - 32 ? launch_cfg<A, OUT, MT, 2, 4>(a, s)
+                                                     : launch_cfg<A, OUT, MT, MT == 4 ? 1 : 2, 4, true>(a, s);
     }
     if (a.N >= 32 * a.cus && a.M > 1) return launch_cfg<A, OUT, MT, MT == 4 && A == MxType::f16 ? 1 : 2, 8>(a, s);
     return launch_cfg<A, OUT, MT, 1, 8>(a, s);
