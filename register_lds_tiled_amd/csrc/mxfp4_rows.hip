@@ -297,12 +297,14 @@ hipError_t launch_mt(const MxGemmArgs& a, hipStream_t s) {
     // One row of 16-bit A takes 256 threads to 32 columns while a launch holds
     // them (N to 2^29 - 32), past that the shared form's 128 (K = 8192, N =
     // 65536: 70 us and 81).
-    if (a.N >= 128 * a.cus) {
-        if constexpr (A == MxType::mxfp4)
-            return launch_cfg<A, OUT, MT, MT == 4 ? 2 : 4, 4>(a, s);
-        else
-            return a.M == 1 && a.N <= (1 << 29) - 32 ? launch_cfg<A, OUT, MT, 2, 4>(a, s)
-                                                     : launch_cfg<A, OUT, MT, MT == 4 ? 1 : 2, 4, true>(a, s);
+    if constexpr (MT == 1) {   // (more than 16 rows come here only where N < 64 CUs)
+        if (a.N >= 128 * a.cus) {
+            if constexpr (A == MxType::mxfp4)
+                return launch_cfg<A, OUT, 1, 4, 4>(a, s);
+            else
+                return a.M == 1 && a.N <= (1 << 29) - 32 ? launch_cfg<A, OUT, 1, 2, 4>(a, s)
+                                                         : launch_cfg<A, OUT, 1, 2, 4, true>(a, s);
+        }
     }
     if (a.N >= 32 * a.cus && a.M > 1) return launch_cfg<A, OUT, MT, MT == 4 && A == MxType::f16 ? 1 : 2, 8>(a, s);
     return launch_cfg<A, OUT, MT, 1, 8>(a, s);

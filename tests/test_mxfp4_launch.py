@@ -62,6 +62,8 @@ hipError_t hipDeviceGetAttribute(int* v, hipDeviceAttribute_t a, int) {
 }
 const char* hipGetErrorName(hipError_t) { return "error"; }
 const char* hipGetErrorString(hipError_t) { return "error"; }
+int record_known() { return (int)names().size(); }
+const char* record_name(int i) { auto it = names().begin(); while (i-- > 0) ++it; return it->second.c_str(); }
 const char* record_kernel() { return kernel.c_str(); }
 unsigned long long record_groups() { return groups; }
 unsigned long long record_threads() { return threads; }
@@ -97,13 +99,13 @@ def lib(tmp_path_factory):
         getattr(lib, f"gemm_mxfp4_{t}").argtypes = [i, i, i, p, i, p, i, p, i, p, i, p, i, p]
     for t in ("bf16", "f16"):
         getattr(lib, f"gemm_{t}_mxfp4_f32").argtypes = [i, i, i, p, i, p, i, p, i, p, i, p]
-    lib.record_kernel.restype = ctypes.c_char_p
+    lib.record_kernel.restype = lib.record_name.restype = ctypes.c_char_p
     lib.record_groups.restype = lib.record_threads.restype = ctypes.c_ulonglong
     return lib
 
 
 TOP = 2 ** 31 - 1
-A, SA, B, SB, C = (0x1000_0000_0000 * n for n in range(1, 6))     # 16 TB apart
+A, SA, B, SB, C, D = (0x1000_0000_0000 * n for n in range(1, 7))     # 16 TB apart
 
 
 def product(lib, kind, M, N, K, pad=0):
@@ -142,3 +144,36 @@ def test_products_launch_or_are_refused(lib, kind, pad):
     for M, N in ((1, WIDE + 1), (1, TOP), (16, TOP), (WIDE + 1, 1), (TOP, 1), (65, WIDE), (100, 64 * 2 ** 23), (TOP, TOP)):
         assert product(lib, kind, M, N, 1, pad) == b.SGEMM_EINVAL_DIM, (M, N)
         assert lib.record_count() == 0
+
+
+def quantise(lib, t, R, C, rows, cols):
+    codes, scales = (-(-C // 2), -(-C // 32)) if rows else (0, 0)
+    codest, scalest = (-(-R // 2), -(-R // 32)) if cols else (0, 0)
+    lib.record_count()
+    return getattr(lib, f"gemm_mxfp4_quantize_{t}")(R, C, A, C, SA if rows else None, codes, B if rows else None, scales,
+                                                    SB if cols else None, codest, D if cols else None, scalest, None)
+
+
+def test_every_kernel_is_launched_by_some_call(lib):
+    """The library holds no MXFP4 kernel that no call reaches."""
+    known = {lib.record_name(i) for i in range(lib.record_known())}
+    assert len(known) > 20
+    reached = set()
+
+    def call(status):
+        assert status == b.SGEMM_OK and lib.record_count() == 1
+        reached.add(lib.record_kernel())
+
+    for kind in KINDS:
+        for M in (1, 2, 16, 17, 32, 33, 64, 65, 1000, 8192):
+            for N in (16, 1000, 8191, 8192, 16383, 16384, 32768, 65536):
+                for pad in (0, 1):
+                    call(product(lib, kind, M, N, 1000, pad))
+    for t in ("f32", "bf16", "f16"):
+        for R, C_ in ((1, 1), (100, 100), (64, 200000), (300, 200000), (8192, 8192)):
+            for rows, cols in ((True, False), (False, True), (True, True)):
+                call(quantise(lib, t, R, C_, rows, cols))
+            for off in (0, 2):
+                call(getattr(lib, f"gemm_mxfp4_dequantize_{t}")(R, C_, SA, -(-C_ // 2), SB, -(-C_ // 32), C + off, C_ + off,
+                                                                None))
+    assert known == reached, sorted(k.decode() for k in known - reached)
