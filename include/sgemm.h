@@ -256,6 +256,9 @@ SGEMM_API int gemm_f16_f32(int M, int N, int K,
  * 6.  Signs are kept, also of zeros.  A block that holds a NaN or an infinity
  * gets scale byte 255, its codes are unspecified.  The last block of a row
  * takes its largest magnitude from the elements that exist.
+ * SGEMM_EINVAL_DIM also for columns asked of an X so large that one workgroup
+ * per 128 x 128 tile (256 threads each) would pass the 2^32 - 1 threads of one
+ * launch.
  * _f32 takes float, _bf16 and _f16 raw 16-bit storage.
  */
 SGEMM_API int gemm_mxfp4_quantize_f32(int R, int C, const void *X, int ldx,

@@ -47,6 +47,10 @@ int quantize(int R, int C, const void* X, int ldx, void* Q, int ldq, void* S, in
     if (X == nullptr || !(rows || cols)) return SGEMM_EINVAL_PTR;
     if (rows && (Q == nullptr || S == nullptr)) return SGEMM_EINVAL_PTR;
     if (cols && (QT == nullptr || ST == nullptr)) return SGEMM_EINVAL_PTR;
+    // Along columns 256 threads per 128 x 128 tile have to fit a launch; along
+    // rows alone the grid is bounded by itself.
+    const long long tiles = ((long long)R + 127) / 128 * (((long long)C + 127) / 128);
+    if (cols && tiles * 256 > 0xFFFFFFFFll) return SGEMM_EINVAL_DIM;
     Ranges g;
     if (rows) {
         g.add(Q, R, value_bytes(C), ldq, 1, true);

@@ -364,26 +364,25 @@ __global__ __launch_bounds__(2 * kTileR) void mx_quantize_both_kernel(MxQuantArg
 }
 
 template <MxType T, int ROWS>
-hipError_t launch_both(const MxQuantArgs& a, long long tn, hipStream_t s) {
-    const long long tm = ((long long)a.R + ROWS - 1) / ROWS;
-    constexpr int NT = 2 * ROWS;
-    if (tm * tn * NT > 0xFFFFFFFFll) return hipErrorInvalidValue;
+hipError_t launch_both(const MxQuantArgs& a, hipStream_t s) {
+    const int tm = (int)(((long long)a.R + ROWS - 1) / ROWS), tn = (int)(((long long)a.C + kTileC - 1) / kTileC);
     if (a.Q != nullptr)
-        mx_quantize_both_kernel<T, true, ROWS><<<(unsigned)(tm * tn), NT, 0, s>>>(a, (int)tm, (int)tn);
+        mx_quantize_both_kernel<T, true, ROWS><<<(unsigned)(tm * tn), 2 * ROWS, 0, s>>>(a, tm, tn);
     else
-        mx_quantize_both_kernel<T, false, ROWS><<<(unsigned)(tm * tn), NT, 0, s>>>(a, (int)tm, (int)tn);
+        mx_quantize_both_kernel<T, false, ROWS><<<(unsigned)(tm * tn), 2 * ROWS, 0, s>>>(a, tm, tn);
     return hipGetLastError();
 }
 
 template <MxType T>
 hipError_t quantize_t(const MxQuantArgs& a, hipStream_t s) {
     if (a.QT != nullptr) {
-        // 256 rows at a time where that leaves two workgroups to a CU: the
-        // transposed codes leave in longer runs (8192^2 bf16 54.9 us against
-        // 57.5, 4096^2 14.2 against 15.6, 8192^2 f32 83 against 82).
-        const long long tn = ((long long)a.C + kTileC - 1) / kTileC;
-        const bool tall = ((long long)a.R + 255) / 256 * tn >= 2 * a.cus;
-        return tall ? launch_both<T, 256>(a, tn, s) : launch_both<T, 128>(a, tn, s);
+        // 256 rows at a time where that leaves two workgroups to a CU (and the
+        // launch holds their 512 threads each): the transposed codes leave in
+        // longer runs (8192^2 bf16 54.9 us against 57.5, 4096^2 14.2 against
+        // 15.6, 8192^2 f32 83 against 82).  128 rows at a time always fit: the
+        // argument checks see to it.
+        const long long tall = ((long long)a.R + 255) / 256 * (((long long)a.C + kTileC - 1) / kTileC);
+        return tall >= 2 * a.cus && tall * 512 <= 0xFFFFFFFFll ? launch_both<T, 256>(a, s) : launch_both<T, 128>(a, s);
     }
     const Items it = items_of(a.R, a.C, 8, kCastItems);
     mx_quantize_rows_kernel<T><<<it.grid, 256, 0, s>>>(a, it.lpr, it.segs, it.items);

@@ -1,5 +1,5 @@
 """GPU tests of the MXFP4 entry points at the ends of their ranges: the widest
-and longest matrices, far rows, and values past what fp32 holds."""
+matrices."""
 import numpy as np
 import pytest
 
@@ -58,3 +58,35 @@ def test_widest_products(M, N):
             fn(M, N, K, x.to(TYPES[name]), K, bq, 1, sb, 1, c, N)
         torch.cuda.synchronize()
         same_in_pieces(c, want, PERIOD)
+
+
+@pytest.mark.parametrize("R,C", [(1, 2 ** 30 - 128), (1, 2 ** 30 + 37), (1, 128 * (2 ** 24 - 1)), (3, 2 ** 30)])
+@pytest.mark.parametrize("rows", [False, True])
+def test_quantise_widest_along_columns(R, C, rows):
+    """Up to 2^31 columns of one to three values each, and the rows with them."""
+    rng = np.random.default_rng(R)
+    period = 4128            # whole blocks of the rows, no multiple of a tile
+    x = torch.from_numpy(rng.standard_normal((R, period)) * np.exp2(rng.integers(-9, 9, (1, period)))).bfloat16()
+    X = repeated(x.view(torch.int16).numpy(), C, 1).contiguous().view(torch.bfloat16)
+    n, m = -(-R // 2), -(-C // 32) if rows else 1
+    qt = torch.full((C, n), 0x5A, dtype=torch.uint8, device=DEV)
+    st = torch.full((C, 1), 0x5A, dtype=torch.uint8, device=DEV)
+    q = torch.full((R, 16 * m), 0x5A, dtype=torch.uint8, device=DEV)
+    s = torch.full((R, m), 0x5A, dtype=torch.uint8, device=DEV)
+    if rows:
+        b.gemm_mxfp4_quantize_bf16(R, C, X, C, q, 16 * m, s, m, qt, n, st, 1)
+    else:
+        b.gemm_mxfp4_quantize_bf16(R, C, X, C, None, 0, None, 0, qt, n, st, 1)
+    torch.cuda.synchronize()
+    x64 = x.double().numpy()
+    codes, byte = mx.quantize(x64.T)
+    want = torch.from_numpy(np.concatenate([mx.pack(codes), byte], 1).T.copy()).to(DEV)
+    same_in_pieces(torch.cat([qt, st], 1).T, want, period)
+    if rows:
+        codes, byte = mx.quantize(x64)
+        full = C // period * period
+        for got, per, k in ((q, torch.from_numpy(mx.pack(codes)).to(DEV), 2), (s, torch.from_numpy(byte).to(DEV), 32)):
+            same_in_pieces(got[:, :full // k], per, period // k)
+        codes, byte = mx.quantize(x64[:, :C - full])
+        assert np.array_equal(s[:, full // 32:].cpu().numpy(), byte)
+        assert np.array_equal(mx.unpack(q[:, full // 2:full // 2 + -(-(C - full) // 2)].cpu().numpy(), C - full), codes)

@@ -177,3 +177,21 @@ def test_every_kernel_is_launched_by_some_call(lib):
                 call(getattr(lib, f"gemm_mxfp4_dequantize_{t}")(R, C_, SA, -(-C_ // 2), SB, -(-C_ // 32), C + off, C_ + off,
                                                                 None))
     assert known == reached, sorted(k.decode() for k in known - reached)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+def test_quantising_launches_or_is_refused(lib, t):
+    """Along columns, up to the last X that one workgroup of 256 threads per
+    128 x 128 tile covers, and beyond it SGEMM_EINVAL_DIM without a launch;
+    along rows any X."""
+    last = 128 * (2 ** 24 - 1)
+    for R, C_ in ((1, 2 ** 30 - 128), (1, 2 ** 30), (1, last), (32, 2 ** 30 + 1), (128, last), (129, 2 ** 30 - 128),
+                  (300, 128 * (2 ** 24 // 3)), (last, 1), (2 ** 30, 128), (2 ** 30 - 128, 129)):
+        for rows in (False, True):
+            assert quantise(lib, t, R, C_, rows, True) == b.SGEMM_OK, (R, C_, lib.record_groups(), lib.record_threads())
+            assert lib.record_count() == 1
+    for R, C_ in ((1, last + 1), (1, TOP), (TOP, 1), (last + 1, 128), (129, 2 ** 30 + 1), (2 ** 30, 129)):
+        for rows in (False, True):
+            assert quantise(lib, t, R, C_, rows, True) == b.SGEMM_EINVAL_DIM, (R, C_)
+            assert lib.record_count() == 0
+        assert quantise(lib, t, R, C_, True, False) == b.SGEMM_OK and lib.record_count() == 1
