@@ -376,13 +376,17 @@ hipError_t launch_both(const MxQuantArgs& a, hipStream_t s) {
 template <MxType T>
 hipError_t quantize_t(const MxQuantArgs& a, hipStream_t s) {
     if (a.QT != nullptr) {
-        // 256 rows at a time where that leaves two workgroups to a CU (and the
-        // launch holds their 512 threads each): the transposed codes leave in
-        // longer runs (8192^2 bf16 54.9 us against 57.5, 4096^2 14.2 against
-        // 15.6, 8192^2 f32 83 against 82).  128 rows at a time always fit: the
-        // argument checks see to it.
+        // 256 rows at a time where there are more than 128 and that leaves two
+        // workgroups to a CU (and the launch holds their 512 threads each): the
+        // transposed codes leave in longer runs.  us both ways, 256 and 128 rows
+        // at a time, bf16: 8192^2 55.5 57.2, 16384 x 4096 55.1 62.6, 256 x 65536
+        // 14.1 14.4, 160 x 262144 36.2 45.5, but 384 x 65536 24.5 22.0; f32:
+        // 8192^2 83.6 82.7, 1024 x 32768 39.5 42.0.  Of at most 128 rows half
+        // the waves and more would have none: 128 x 65536 10.8 8.5, 1 x 10^6 83
+        // 46.  128 rows at a time always fit: the argument checks see to it.
         const long long tall = ((long long)a.R + 255) / 256 * (((long long)a.C + kTileC - 1) / kTileC);
-        return tall >= 2 * a.cus && tall * 512 <= 0xFFFFFFFFll ? launch_both<T, 256>(a, s) : launch_both<T, 128>(a, s);
+        return a.R > 128 && tall >= 2 * a.cus && tall * 512 <= 0xFFFFFFFFll ? launch_both<T, 256>(a, s)
+                                                                            : launch_both<T, 128>(a, s);
     }
     const Items it = items_of(a.R, a.C, 8, kCastItems);
     mx_quantize_rows_kernel<T><<<it.grid, 256, 0, s>>>(a, it.lpr, it.segs, it.items);

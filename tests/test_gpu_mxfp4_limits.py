@@ -5,6 +5,7 @@ import pytest
 
 from oracle import mxfp4 as mx
 from register_lds_tiled_amd import binding as b
+from tests.test_gpu_mxfp4 import quantize_case
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -90,3 +91,11 @@ def test_quantise_widest_along_columns(R, C, rows):
         codes, byte = mx.quantize(x64[:, :C - full])
         assert np.array_equal(s[:, full // 32:].cpu().numpy(), byte)
         assert np.array_equal(mx.unpack(q[:, full // 2:full // 2 + -(-(C - full) // 2)].cpu().numpy(), C - full), codes)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("R,C", [(33, 66001), (128, 65664), (129, 66001), (300, 40001), (2100, 7500)])
+def test_quantise_in_tiles_of_either_height(t, R, C):
+    """Shapes beside the choice between tiles of 128 and 256 rows, odd ends."""
+    quantize_case(t, R, C, False, True)
+    quantize_case(t, R, C, True, True)

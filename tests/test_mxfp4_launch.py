@@ -195,3 +195,15 @@ def test_quantising_launches_or_is_refused(lib, t):
             assert quantise(lib, t, R, C_, rows, True) == b.SGEMM_EINVAL_DIM, (R, C_)
             assert lib.record_count() == 0
         assert quantise(lib, t, R, C_, True, False) == b.SGEMM_OK and lib.record_count() == 1
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+def test_quantising_few_rows_leaves_no_wave_idle(lib, t):
+    """A tile of 256 rows for at most 128 would leave half of its waves and more
+    without any; from there on it is taken where it fills the CUs."""
+    for R, threads in ((1, 256), (32, 256), (128, 256), (129, 512), (256, 512)):
+        for rows in (False, True):
+            assert quantise(lib, t, R, 65536, rows, True) == b.SGEMM_OK
+            assert lib.record_threads() == threads, (R, rows)
+            assert quantise(lib, t, R, 65408, rows, True) == b.SGEMM_OK     # 511 tiles for 256 CUs
+            assert lib.record_threads() == 256, (R, rows)
