@@ -218,7 +218,7 @@ SGEMM_API int gemm_f16_f32(int M, int N, int K,
  * Microscaled 4-bit floating point (MXFP4): the element and block formats of
  * the OCP Microscaling Formats (MX) specification 1.0, E2M1 elements in blocks
  * of 32 with an E8M0 scale, multiplied on the matrix cores
- * (v_mfma_scale_f32_16x16x128_f8f6f4).
+ * (v_mfma_scale_f32_32x32x64_f8f6f4; for few rows 16x16x128).
  *
  * An MXFP4 matrix of R rows and K columns is two byte matrices:
  * - values Q: row r's ceil(K/2) bytes at Q + r*ldq.  Byte i holds element 2i
@@ -290,9 +290,16 @@ SGEMM_API int gemm_mxfp4_dequantize_f16(int R, int C, const void *Q, int ldq,
 /*
  * C = A.B^T with A (M x K) and B (N x K) in MXFP4, both blocked along K:
  *     C[i,j] = sum_k A[i,k] * B[j,k]
- * accumulated in fp32 (products with their scales are exact there), C fp32 or
- * bfloat16 (rounded once, to nearest even).  B's rows are the product's
- * columns: a layer's weights, outputs x inputs, are used as they are stored.
+ * accumulated in fp32, C fp32 or bfloat16 (rounded once, to nearest even).  B's
+ * rows are the product's columns: a layer's weights, outputs x inputs, are used
+ * as they are stored.
+ * Products of two elements with their scales have few significant bits: those
+ * that fp32's normal range holds are exact, and where it holds them all and
+ * their sums the result is within the fp32 rounding of some summation order.
+ * Scales reach past that range both ways (2^-254 to 2^254): a product or
+ * partial sum below 2^-126 in magnitude may lose bits, down to all of them
+ * (each then adds an error of at most 2^-126); one past the largest fp32
+ * number is infinite, and infinities of both signs make NaN.
  * The three products of a linear layer Y = X.W^T are
  *     Y  = A.B^T of X and W, each quantised along its rows,
  *     dX = A.B^T of dY (rows) and W (columns: its QT, ST),
@@ -311,10 +318,11 @@ SGEMM_API int gemm_mxfp4_bf16(int M, int N, int K,
 /*
  * C = A.B^T with 16-bit A (M x K, row-major, lda in elements) and B (N x K) in
  * MXFP4 blocked along K, fp32 accumulate and C: weights kept in four bits,
- * activations as they are.  Products are exact in fp32, so the result is
- * within the fp32 rounding of some summation order of the exact products.  An
- * element of B of magnitude 2^128 or more (possible at scale bytes 253 and
- * above) makes the outputs it contributes to infinite or NaN.  K == 0 stores zeros.  M of at most 64 streams B once.
+ * activations as they are.  Products that fp32's normal range holds are exact;
+ * beyond it, either way, gemm_mxfp4_f32's rule holds, except that a binary16
+ * A's product may lose 2^-126 twice.  An element of B of magnitude 2^128 or
+ * more (possible at scale bytes 253 and above) makes the outputs it contributes
+ * to infinite or NaN.  K == 0 stores zeros.  M of at most 64 streams B once.
  */
 SGEMM_API int gemm_bf16_mxfp4_f32(int M, int N, int K,
                         const void *A, int lda,

@@ -1,11 +1,18 @@
 """GPU tests of the MXFP4 entry points at the ends of their ranges: the widest
-matrices."""
+matrices, and products that fp32 does not hold.
+
+Products below fp32's normal range may lose bits down to all of them: each of
+the passes * K terms and of the T partial sums (T as derived in
+test_gpu_mxfp4.py) is then off by at most 2^-126 more, so
+    |C - R| <= T 2^-23 S + (passes * K + T) 2^-126.
+Where all terms are positive, a sum R with R (1 - T 2^-23) above the largest
+fp32 number is infinite."""
 import numpy as np
 import pytest
 
 from oracle import mxfp4 as mx
 from register_lds_tiled_amd import binding as b
-from tests.test_gpu_mxfp4 import quantize_case
+from tests.test_gpu_mxfp4 import Bytes, as_type, operand, quantize_case, run_product, run_wproduct
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -99,3 +106,78 @@ def test_quantise_in_tiles_of_either_height(t, R, C):
     """Shapes beside the choice between tiles of 128 and 256 rows, odd ends."""
     quantize_case(t, R, C, False, True)
     quantize_case(t, R, C, True, True)
+
+
+# ---- products that fp32 does not hold ---------------------------------------
+
+FORMS = [(1, 150, 416), (20, 150, 416), (140, 150, 416), (16, 40, 1000), (300, 300, 700)]
+
+
+def check_range(C, A, B, out, step, passes):
+    """C against the exact sums, whose terms may leave fp32's range."""
+    K = A.shape[1]
+    R, S = mx.product(A, B)
+    T = passes * -(-K // step) + 32
+    tol = T * 2.0 ** -23 * S + (passes * K + T) * 2.0 ** -126
+    if out == "bf16":
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(R)
+    high = R * (1 - T * 2.0 ** -23) > np.finfo(np.float32).max
+    # (bfloat16 rounds to an infinity from half a step below 2^128 on)
+    edge = ~high & (S * (1 + T * 2.0 ** -23) >= (2.0 ** 128 - 2.0 ** 119 if out == "bf16" else 2.0 ** 128))
+    assert (C[high] == np.inf).all()
+    mid = ~high & ~edge
+    bad = ~(np.abs(C - R) <= tol)[mid]
+    assert not bad.any(), (bad.sum(), C[mid][bad][:4], R[mid][bad][:4], tol[mid][bad][:4])
+    return high, mid
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_products_beyond_fp32(out, pad, M, N, K):
+    rng = np.random.default_rng(M + pad)
+    n = (-((K + 1) // 2)) % 16 + pad
+    for (alo, ahi), (blo, bhi) in (((0, 3), (0, 3)), ((40, 80), (50, 90)), ((0, 60), (60, 80)), ((60, 70), (58, 66)), ((54, 64), (54, 62))):
+        a, sa, A = operand(rng, M, K, alo, ahi, pad=n)
+        w, sw, W = operand(rng, N, K, blo, bhi, pad=n)
+        high, mid = check_range(run_product(out, M, N, K, a, sa, w, sw), A, W, out, 64, 1)
+        assert mid.all()
+    seen = []
+    for (alo, ahi), (blo, bhi) in (((253, 255), (253, 255)), ((185, 193), (180, 192)), ((200, 255), (120, 200)), ((178, 186), (174, 186))):
+        a, sa, A = operand(rng, M, K, alo, ahi, pad=n)
+        w, sw, W = operand(rng, N, K, blo, bhi, pad=n)
+        for o in (a, w):                              # no minus signs
+            o.host &= 0x77
+            o.dev.copy_(torch.from_numpy(o.host))
+        C = run_product(out, M, N, K, a, sa, w, sw)
+        seen.append(check_range(C, np.abs(A), np.abs(W), out, 64, 1)[0].any())
+    assert any(seen)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_weight_products_beyond_fp32(t, pad, M, N, K):
+    rng = np.random.default_rng(M + pad)
+    n = (-((K + 1) // 2)) % 16 + pad
+    lda = K + (-K) % 8 + pad
+
+    def a16(x):
+        raw, A = as_type(x, t)
+        return Bytes(M, 2 * K, 2 * lda, 0, 0xFF, raw), A
+
+    small = {"bf16": (((0, 3), -130), ((20, 60), -60), ((60, 70), -66)), "f16": (((0, 3), -18), ((0, 12), -8))}[t]
+    for (lo, hi), e in small:
+        a, A = a16(rng.standard_normal((M, K)) * 2.0 ** e)
+        w, sw, W = operand(rng, N, K, lo, hi, pad=n)
+        high, mid = check_range(run_wproduct(t, M, N, K, a, lda, w, sw), A, W, "f32", 16, 2)
+        assert mid.all()
+    seen = []
+    large = {"bf16": (((200, 252), 60), ((180, 190), 70), ((170, 180), 68)), "f16": (((240, 252), 12), ((238, 246), 8), ((232, 240), 8))}[t]
+    for (lo, hi), e in large:
+        a, A = a16(np.abs(rng.standard_normal((M, K))) * 2.0 ** e)
+        w, sw, W = operand(rng, N, K, lo, hi, pad=n)
+        w.host &= 0x77
+        w.dev.copy_(torch.from_numpy(w.host))
+        seen.append(check_range(run_wproduct(t, M, N, K, a, lda, w, sw), A, np.abs(W), "f32", 16, 2)[0].any())
+    assert any(seen)
