@@ -1,5 +1,5 @@
 """GPU tests of the MXFP4 entry points at the ends of their ranges: the widest
-matrices, and products that fp32 does not hold.
+matrices, far rows, and products that fp32 does not hold.
 
 Products below fp32's normal range may lose bits down to all of them: each of
 the passes * K terms and of the T partial sums (T as derived in
@@ -12,7 +12,7 @@ import pytest
 
 from oracle import mxfp4 as mx
 from register_lds_tiled_amd import binding as b
-from tests.test_gpu_mxfp4 import Bytes, as_type, operand, quantize_case, run_product, run_wproduct
+from tests.test_gpu_mxfp4 import Bytes, as_type, check_product, operand, quantize_case, run_product, run_wproduct
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -181,3 +181,23 @@ def test_weight_products_beyond_fp32(t, pad, M, N, K):
         w.dev.copy_(torch.from_numpy(w.host))
         seen.append(check_range(run_wproduct(t, M, N, K, a, lda, w, sw), A, np.abs(W), "f32", 16, 2)[0].any())
     assert any(seen)
+
+
+# ---- far rows ---------------------------------------------------------------
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_wide_tiles_of_far_rows(out):
+    """256 x 256 tiles whose rows of B lie past 2^31 bytes from their first, up
+    to the last pitch that 32-bit offsets reach."""
+    M, N, K, pitch = 32800, 256, 320, (16 << 20) - 16
+    rng = np.random.default_rng(1)
+    a, sa, A = operand(rng, M, K)
+    w, sw, W = operand(rng, N, K)
+    big = torch.full((N * pitch,), 0x77, dtype=torch.uint8, device=DEV)
+    rows = torch.arange(N, device=DEV)[:, None] * pitch + torch.arange(K // 2, device=DEV)
+    big[rows] = torch.from_numpy(w.view(w.host)[:, :K // 2].copy()).to(DEV)
+    c = torch.full((M, N), float("nan"), dtype=TYPES[out], device=DEV)
+    fn = b.gemm_mxfp4_f32 if out == "f32" else b.gemm_mxfp4_bf16
+    fn(M, N, K, a.ptr, a.ld, sa.ptr, sa.ld, big, pitch, sw.ptr, sw.ld, c, N)
+    torch.cuda.synchronize()
+    check_product(c.double().cpu().numpy(), A, W, out, 64, what=f"far rows, {out}")
