@@ -288,6 +288,11 @@ def _mx_setup():
     _torch = torch
 
 
+def _no_c_int(name, n):
+    """ctypes would pass such an integer's lowest 32 bits, another size."""
+    raise OverflowError(f"{name}: {n} does not fit the library's int")
+
+
 def _mx_call(name, head, operands, stream, check):
     """One MXFP4 entry point: `head` its leading integers, `operands` (kind,
     address or tensor or None, leading dimension) in the C order.  Tensors lie
@@ -297,7 +302,12 @@ def _mx_call(name, head, operands, stream, check):
         _mx_setup()
     tensor = _torch.Tensor
     args, dev = list(head), None
+    for n in head:
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
+            _no_c_int(name, n)
     for kind, x, ld in operands:
+        if not -0x80000000 <= ld <= 0x7FFFFFFF:
+            _no_c_int(name, ld)
         if isinstance(x, tensor):
             if x.dtype not in _MX_KINDS[kind]:
                 raise TypeError(f"{name}: a {kind} operand cannot be a {x.dtype} tensor")
