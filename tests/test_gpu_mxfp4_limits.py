@@ -201,3 +201,49 @@ def test_wide_tiles_of_far_rows(out):
     fn(M, N, K, a.ptr, a.ld, sa.ptr, sa.ld, big, pitch, sw.ptr, sw.ld, c, N)
     torch.cuda.synchronize()
     check_product(c.double().cpu().numpy(), A, W, out, 64, what=f"far rows, {out}")
+
+
+# ---- long rows --------------------------------------------------------------
+
+# K at the last row length that the kernels' 32-bit row offsets reach and past
+# it: few rows (64 rows of B), MXFP4 tiles (256 rows), 16-bit tiles (128 rows)
+LONGEST = [("few", 2, 2 ** 27 - 32), ("few", 2, 2 ** 27 + 33), ("tile", 66, 2 ** 25 - 32), ("tile", 66, 2 ** 25 + 33),
+           ("tile16", 66, 2 ** 24 - 8), ("tile16", 66, 2 ** 24 + 9)]
+
+
+@pytest.mark.parametrize("form,M,K", LONGEST)
+def test_longest_rows(form, M, K):
+    """A few hundred whole numbers among zeros, the row's ends with them."""
+    N = 5
+    rng = np.random.default_rng(K % 1000)
+    at = np.unique(np.concatenate([rng.integers(0, K, 300), [0, 1, 31, 32, K - 1, K - 2, K - 33]]))
+    ld, ls = -(-K // 32) * 16, -(-K // 32)
+
+    def sparse(rows):
+        codes = rng.integers(0, 16, (rows, at.size))
+        q = torch.zeros((rows, ld), dtype=torch.uint8, device=DEV)
+        low, high = at % 2 == 0, at % 2 == 1
+        q[:, torch.from_numpy(at[low] // 2).to(DEV)] = torch.from_numpy(codes[:, low].astype(np.uint8)).to(DEV)
+        q[:, torch.from_numpy(at[high] // 2).to(DEV)] |= torch.from_numpy((codes[:, high] << 4).astype(np.uint8)).to(DEV)
+        s = torch.from_numpy(rng.integers(125, 130, (rows, ls), dtype=np.uint8)).to(DEV)
+        byte = s[:, torch.from_numpy(at // 32).to(DEV)].cpu().numpy()
+        return q, s, mx.element(codes) * mx.scale(byte)
+
+    w, sw, W = sparse(N)
+    c = torch.full((M, N), float("nan"), device=DEV)
+    if form != "tile16":
+        a, sa, A = sparse(M)
+        b.gemm_mxfp4_f32(M, N, K, a, ld, sa, ls, w, ld, sw, ls, c, N)
+        torch.cuda.synchronize()
+        assert np.array_equal(c.double().cpu().numpy(), A @ W.T)
+        del a, sa
+    if form != "tile":
+        lda = K + (-K) % 8
+        for t, fn in (("bf16", b.gemm_bf16_mxfp4_f32), ("f16", b.gemm_f16_mxfp4_f32)):
+            A = rng.integers(-8, 9, (M, at.size)).astype(np.float64)
+            x = torch.zeros((M, lda), dtype=TYPES[t], device=DEV)
+            x[:, torch.from_numpy(at).to(DEV)] = torch.from_numpy(A).to(DEV, TYPES[t])
+            c.fill_(float("nan"))
+            fn(M, N, K, x, lda, w, ld, sw, ls, c, N)
+            torch.cuda.synchronize()
+            assert np.array_equal(c.double().cpu().numpy(), A @ W.T), t
