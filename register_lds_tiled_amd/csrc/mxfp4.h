@@ -67,7 +67,7 @@ hipError_t launch_mx_gemm(const MxGemmArgs& a, MxType out, hipStream_t s);
 // t: the type of A, bf16 or f16; C is fp32.
 hipError_t launch_mx_wgemm(const MxGemmArgs& a, MxType t, hipStream_t s);
 
-// Both products for at most 64 rows of A, whose type is a_type (mxfp4, bf16 or
+// Both products where mx_few_rows says so; A's type is a_type (mxfp4, bf16 or
 // f16); C's type is out (f32, or bf16 where A is mxfp4).
 hipError_t launch_mx_rows(const MxGemmArgs& a, MxType a_type, MxType out, hipStream_t s);
 
@@ -170,9 +170,9 @@ __device__ __forceinline__ uint4 mx_keep(uint4 v, int left) {
 inline bool mx_dma_reach(long long ld_bytes, int rows) { return ld_bytes * rows < (1ll << 32); }
 // Whether a product takes the few-row kernel: at most 16 rows, or at most 64
 // where 128 x 128 tiles would leave half the CUs idle (64 rows, K = 8192: N =
-// 8192 takes 18 us in the few-row kernel and 34 in tiles, 24576 54 and 39; with
-// 16-bit A 34 and 62, 100 and 66); and 64 rows of every operand in reach of
-// 32-bit offsets.
+// 8192 takes 19 us in the few-row kernel and 34 in tiles, 16128 37 and 36, 24576
+// 54 and 41; with bfloat16 A 35 and 63, 69 and 64, 100 and 66); and 64 rows of
+// every operand in reach of 32-bit offsets.
 inline bool mx_few_rows(const MxGemmArgs& a) {
     return (a.M <= 16 || (a.M <= 64 && 2 * (((long long)a.N + 127) / 128) < a.cus)) && mx_dma_reach(a.lda, 64) &&
            mx_dma_reach(a.ldsa, 64) && mx_dma_reach(a.ldb, 64) && mx_dma_reach(a.ldsb, 64);
@@ -290,9 +290,9 @@ __device__ __forceinline__ void store4(const MxGemmArgs& p, long long row, long 
 }
 
 // A wave's outputs from 32 x 32 accumulators, the first of them (r0, c0).  fp32
-// rows on whole lines stream past the caches (8192^3 283 us against 300); others
+// rows on whole lines stream past the caches (8192^3 277 us against 288); others
 // do not, as their pieces of a line meet only there (6336 x 4669 x 90 44 us
-// against 62).
+// against 64).
 template <MxType OUT, int FM, int FN>
 __device__ __forceinline__ void mx_store_wave(const MxGemmArgs& p, const floatx16 (&acc)[FM][FN], long long r0,
                                               long long c0, int li, int g) {

@@ -1,11 +1,11 @@
 // mxfp4_gemm.hip -- C = A.B^T with both operands in MXFP4, on the matrix
 // cores, accumulated in fp32.
 //
-// At most 64 rows of A: mxfp4_rows.hip.  Else tiles: 256 x 256 and 128 x 128 by
-// DMA, 128 x 128 through registers where rows are not 16-byte aligned.  8192^3
-// takes 273 us to fp32 C and 263 to bfloat16 (4.0 and 4.2 PFLOP/s); the matrix
-// instructions alone would need 164 on random codes, where power limits them,
-// and 112 on zeros.
+// Few rows of A (at most 16, or 64 where C is narrow: mx_few_rows):
+// mxfp4_rows.hip.  Else tiles: 256 x 256 and 128 x 128 by DMA, 128 x 128 through
+// registers where rows are not 16-byte aligned.  8192^3 takes 277 us to fp32 C
+// and 272 to bfloat16 (4.0 PFLOP/s); the matrix instructions alone would need
+// 164 on random codes, where power limits them, and 115 on zeros.
 #include "mxfp4.h"
 
 namespace sgemm {
@@ -170,7 +170,8 @@ __global__ __launch_bounds__(Cfg::NT) void mx_tile_kernel(MxGemmArgs p, int tile
 // of row r at c ^ (r / 4 & 3).  They are read along the rows while the last
 // stage that needs the ones before multiplies, and written after it.  (Loaded
 // straight to the lanes that need them, a row a lane, they took the address
-// unit as long as half the codes: 8192^3 to bf16 369 us, 307 without.)
+// unit as long as half the codes: 8192^3 to bf16 in 128 x 128 tiles 369 us, 307
+// without any scales.)
 //
 // Past K: a chunk that begins past a row's end is read from the row's last
 // one, and what is past K in A's last stage is cleared in LDS; B's codes
@@ -373,10 +374,11 @@ hipError_t launch_out(const MxGemmArgs& a, hipStream_t s) {
                      mx_dma_reach(a.lda, 256) && mx_dma_reach(a.ldb, 256);
     if (!dma) return launch_tile<MxTile<128, 128, 64, 64>, OUT>(a, s);
     // Rounds of workgroups, one 256 x 256 or two 128 x 128 to a CU, times what a
-    // round takes (8192^3: 71 us of four rounds, 43 of eight).  The wide tiles
-    // read half as much through L2, whose rate (25 TB/s and more) bounds the
-    // others: 8192^3 297 against 330 us, 4096 x 8192 x 4096 83 against 100;
-    // 2048^3, 64 wide tiles, 20 against 11.
+    // round takes (8192^3: 69 us of four rounds, 39 to 41 of eight).  The wide
+    // tiles read half as much through L2, whose rate (25 TB/s and more) bounds
+    // the others.  us to fp32 and bfloat16: 8192^3 277 and 272 wide, 310 and 329
+    // else; 4096 x 8192 x 4096 91 and 78, 92 and 97; 2048^3, 64 wide tiles, to
+    // bfloat16 20 against 11.
     const long long wide = ((long long)a.M + 255) / 256 * (((long long)a.N + 255) / 256);
     const long long small = ((long long)a.M + 127) / 128 * (((long long)a.N + 127) / 128);
     if (5 * ((wide + a.cus - 1) / a.cus) <= 3 * ((small + 2 * a.cus - 1) / (2 * a.cus)))

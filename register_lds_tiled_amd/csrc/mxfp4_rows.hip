@@ -1,5 +1,6 @@
-// mxfp4_rows.hip -- C = A.B^T for at most 64 rows of A (a token, or a batch of
-// them, in decoding) and MXFP4 B: B is streamed once, A is MXFP4 or 16-bit.
+// mxfp4_rows.hip -- C = A.B^T for few rows of A (a token, or a batch of them, in
+// decoding: at most 16, or 64 where C is narrow, see mx_few_rows) and MXFP4 B:
+// B is streamed once, A is MXFP4 or 16-bit.
 //
 // Bound by memory: half a byte of codes and 1/32 of scales per element of B,
 // and the latency of asking for them.  A workgroup owns 16 NT columns of C
@@ -287,16 +288,18 @@ hipError_t launch_cfg(const MxGemmArgs& a, hipStream_t s) {
 template <MxType A, MxType OUT, int MT>
 hipError_t launch_mt(const MxGemmArgs& a, hipStream_t s) {
     // More columns to a workgroup read A less often, fewer leave more
-    // workgroups.  us at K = 8192, N = 65536 and 8192:
-    //                            MXFP4 A: one row   16 rows   16-bit A: one row   16 rows
-    //   16 columns, 8 waves         59.8  10.3   78.1  11.9       70.9  12.0    121  17.8
-    //   32 columns, 8 waves         59.7  10.3   74.8  11.7       73.1  12.5    108  16.0
-    //   64 columns, 4 waves         56.3  15.1   63.8  17.3       67.6  19.7     99  24.5
-    //   4 x 32 columns, A shared                                  75.6           82
-    // (At N = K = 1024 16 columns take 2.7, 32 take 3.0.)
+    // workgroups.  us at K = 8192, N = 65536 and 8192 (binary16 A: 65536 and, of
+    // 16 rows, 8192):
+    //                           MXFP4 A            bfloat16 A          binary16 A
+    //                      one row    16 rows   one row   16 rows    one   16 rows
+    //   16 columns, 8 waves  60 11.0   79 12.5   73 12.3  119 17.9    72   121 18.2
+    //   32 columns, 8 waves  60 10.9   74 12.1   73 12.7  106 16.2    77   108 16.6
+    //   32 columns, 4 waves  60 12.7   71 14.8   68 15.0   98 20.4    72   102 20.9
+    //   64 columns, 4 waves  57 15.0   64 17.3   67 19.7   83 24.4    83   120 28.2
+    //   4 x 32, A shared                         75 45.5   84 47.5    74    82 49.0
+    // (N = K = 1024: 16 columns 2.7, 32 columns 3.0.)
     // One row of 16-bit A takes 256 threads to 32 columns while a launch holds
-    // them (N to 2^29 - 32), past that the shared form's 128 (K = 8192, N =
-    // 65536: 70 us and 81).
+    // them (N to 2^29 - 32), past that the shared form's 128.
     if constexpr (MT == 1) {   // (more than 16 rows come here only where N < 64 CUs)
         if (a.N >= 128 * a.cus) {
             if constexpr (A == MxType::mxfp4)

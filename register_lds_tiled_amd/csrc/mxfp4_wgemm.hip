@@ -4,17 +4,19 @@
 // An MXFP4 value has at most two significant bits and an exponent between
 // -128 and 129, so bfloat16 holds it exactly (2^128 and beyond as infinity):
 // B's codes become bfloat16 in registers (v_cvt_scalef32_pk_bf16_fp4, two
-// elements with their scale) and multiply in v_mfma_f32_16x16x32_bf16.
-// binary16 A: where binary16 holds every value of the blocks at hand (scale
-// bytes 104 to 140, any usual weight), they become binary16 and multiply in
-// v_mfma_f32_16x16x32_f16.  Where it does not, A splits exactly into two
-// bfloat16 terms, hi + lo (11 significant bits in 8 + 8), and both multiply
-// the same bfloat16 B.
+// elements with their scale) and multiply in v_mfma_f32_32x32x16_bf16 (16x16x32
+// where rows are few or off 16 bytes).  binary16 A: where binary16 holds every
+// value of the blocks at hand (scale bytes 104 to 140, any usual weight), they
+// become binary16 and multiply in the same instructions' _f16 forms.  Where it
+// does not, A splits exactly into two bfloat16 terms, hi + lo (11 significant
+// bits in 8 + 8), and both multiply the same bfloat16 B.
 //
-// At most 64 rows of A: mxfp4_rows.hip.  Else 128 x 128 tiles, by DMA where rows
-// are 16-byte aligned: 4096 x 8192 x 8192 takes 453 us (1.21 PFLOP/s), 518 with
-// binary16 A; the product of two bfloat16 matrices, whose 1.35 to 1.42 PFLOP/s
-// power bounds, has no conversions to do.
+// Few rows of A (at most 16, or 64 where C is narrow: mx_few_rows):
+// mxfp4_rows.hip.  Else 128 x 128 tiles, by DMA where rows are 16-byte aligned:
+// 4096 x 8192 x 8192 takes 454 us (1.21 PFLOP/s), 521 with binary16 A, whose
+// loop differs by a vote and a branch on the scales' range in every half stage;
+// the product of two bfloat16 matrices, whose 1.35 to 1.42 PFLOP/s power bounds,
+// has no conversions to do.
 #include "mxfp4.h"
 
 namespace sgemm {

@@ -2,8 +2,9 @@
 
 Quantising and reading back must match bit for bit: the scale is an exponent,
 and rounding to a code is exact.  Products: every product of two elements with
-their scales is exact in fp32 (at most 4 significant bits, or 2 + 11), so C
-differs from the exact sum only by the additions.  The matrix cores add 64
+their scales that fp32's normal range holds is exact there (at most 4 significant
+bits, or 2 + 11), so C differs from the exact sum only by the additions.  The
+matrix cores add 64
 (16-bit A: 16 at least, and binary16 A takes two passes) products at a time into
 an fp32 accumulator, and the sum over k may be split among up to 16 waves whose
 parts are then added: for each output at most
@@ -672,8 +673,9 @@ def test_large_offsets():
     same(Y[R - 200:].double().cpu().numpy(), q64(X64), "read back")
     assert int((Y[:R - 200] != 0).sum()) == 0
     del X, Y, qt, st
-    # a product whose second operand's last rows lie past 2^32 bytes of row pitch
-    # (few rows; tiles whose rows 32-bit offsets reach, past 2^31, and do not)
+    # a product whose second operand's last rows lie past 2^32 bytes of row pitch:
+    # few rows; the 16-bit tiles' DMA, by offsets past 2^31 (24 MiB), and beyond
+    # its reach (40 MiB); the MXFP4 tiles, beyond their DMA's reach in all three
     N, K = 300, 512
     bq, sb, B = operand(np.random.default_rng(1), N, K)
     for M, pitch in ((2, 16 << 20), (100, 16 << 20), (100, 24 << 20), (100, 40 << 20)):
