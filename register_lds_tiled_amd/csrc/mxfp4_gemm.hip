@@ -36,8 +36,8 @@ __device__ __forceinline__ floatx16 mfma_mx32(uint4 a, unsigned sa, uint4 b, uns
 // together.  In the operand reads these are as many rows of one chunk, rows of
 // one parity share half of the banks, and r / 2 mod 8 is different for all rows
 // of one parity in either set.  (With r mod 8 half of all LDS cycles were bank
-// conflicts; this way these reads have none.  A quarter remains in the wide
-// tiles, from the scales' 4-byte reads.)
+// conflicts; this way these reads have none.  A quarter remains, from the
+// scales' 4-byte reads.)
 __device__ __forceinline__ int place_of(int r) { return r >> 1 & 7; }
 
 template <int BM_, int BN_, int WM_, int WN_, int OCC_ = 1, int GROUP_M_ = 8>
