@@ -299,7 +299,8 @@ SGEMM_API int gemm_mxfp4_dequantize_f16(int R, int C, const void *Q, int ldq,
  * Scales reach past that range both ways (2^-254 to 2^254): a product or
  * partial sum below 2^-126 in magnitude may lose bits, down to all of them
  * (each then adds an error of at most 2^-126); one past the largest fp32
- * number is infinite, and infinities of both signs make NaN.
+ * number may become infinite (it does where all terms have one sign), and
+ * infinities of both signs make NaN.
  * The three products of a linear layer Y = X.W^T are
  *     Y  = A.B^T of X and W, each quantised along its rows,
  *     dX = A.B^T of dY (rows) and W (columns: its QT, ST),

@@ -296,8 +296,8 @@ def _no_c_int(name, n):
 def _mx_call(name, head, operands, stream, check):
     """One MXFP4 entry point: `head` its leading integers, `operands` (kind,
     address or tensor or None, leading dimension) in the C order, all of them
-    within a C int's range.  Tensors lie on one device, whose current stream is the default and which is the
-    current device during the call."""
+    within a C int's range.  Tensors lie on one device, whose current stream is
+    the default and which is the current device during the call."""
     if _torch is None:
         _mx_setup()
     tensor = _torch.Tensor

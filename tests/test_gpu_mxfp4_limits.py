@@ -137,13 +137,15 @@ def check_range(C, A, B, out, step, passes):
 def test_products_beyond_fp32(out, pad, M, N, K):
     rng = np.random.default_rng(M + pad)
     n = (-((K + 1) // 2)) % 16 + pad
-    for (alo, ahi), (blo, bhi) in (((0, 3), (0, 3)), ((40, 80), (50, 90)), ((0, 60), (60, 80)), ((60, 70), (58, 66)), ((54, 64), (54, 62))):
+    for (alo, ahi), (blo, bhi) in (((0, 3), (0, 3)), ((40, 80), (50, 90)), ((0, 60), (60, 80)), ((60, 70), (58, 66)),
+                                   ((54, 64), (54, 62))):
         a, sa, A = operand(rng, M, K, alo, ahi, pad=n)
         w, sw, W = operand(rng, N, K, blo, bhi, pad=n)
         high, mid = check_range(run_product(out, M, N, K, a, sa, w, sw), A, W, out, 64, 1)
         assert mid.all()
     seen = []
-    for (alo, ahi), (blo, bhi) in (((253, 255), (253, 255)), ((185, 193), (180, 192)), ((200, 255), (120, 200)), ((178, 186), (174, 186))):
+    for (alo, ahi), (blo, bhi) in (((253, 255), (253, 255)), ((185, 193), (180, 192)), ((200, 255), (120, 200)),
+                                   ((178, 186), (174, 186))):
         a, sa, A = operand(rng, M, K, alo, ahi, pad=n)
         w, sw, W = operand(rng, N, K, blo, bhi, pad=n)
         for o in (a, w):                              # no minus signs
@@ -173,7 +175,8 @@ def test_weight_products_beyond_fp32(t, pad, M, N, K):
         high, mid = check_range(run_wproduct(t, M, N, K, a, lda, w, sw), A, W, "f32", 16, 2)
         assert mid.all()
     seen = []
-    large = {"bf16": (((200, 252), 60), ((180, 190), 70), ((170, 180), 68)), "f16": (((240, 252), 12), ((238, 246), 8), ((232, 240), 8))}[t]
+    large = {"bf16": (((200, 252), 60), ((180, 190), 70), ((170, 180), 68)),
+             "f16": (((240, 252), 12), ((238, 246), 8), ((232, 240), 8))}[t]
     for (lo, hi), e in large:
         a, A = a16(np.abs(rng.standard_normal((M, K))) * 2.0 ** e)
         w, sw, W = operand(rng, N, K, lo, hi, pad=n)

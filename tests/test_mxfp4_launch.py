@@ -141,7 +141,8 @@ def test_products_launch_or_are_refused(lib, kind, pad):
     for M, N in ((WIDE, 1), (WIDE, 64), (64, WIDE), (64 * 4095, 64 * 4096), (100, 64 * (2 ** 23 - 1))):
         assert product(lib, kind, M, N, 32, pad) == b.SGEMM_OK, (M, N, lib.record_kernel(), lib.record_groups())
         assert lib.record_count() == 1
-    for M, N in ((1, WIDE + 1), (1, TOP), (16, TOP), (WIDE + 1, 1), (TOP, 1), (65, WIDE), (100, 64 * 2 ** 23), (TOP, TOP)):
+    for M, N in ((1, WIDE + 1), (1, TOP), (16, TOP), (WIDE + 1, 1), (TOP, 1), (65, WIDE), (100, 64 * 2 ** 23),
+                 (TOP, TOP)):
         assert product(lib, kind, M, N, 1, pad) == b.SGEMM_EINVAL_DIM, (M, N)
         assert lib.record_count() == 0
 
@@ -174,8 +175,8 @@ def test_every_kernel_is_launched_by_some_call(lib):
             for rows, cols in ((True, False), (False, True), (True, True)):
                 call(quantise(lib, t, R, C_, rows, cols))
             for off in (0, 2):
-                call(getattr(lib, f"gemm_mxfp4_dequantize_{t}")(R, C_, SA, -(-C_ // 2), SB, -(-C_ // 32), C + off, C_ + off,
-                                                                None))
+                fn = getattr(lib, f"gemm_mxfp4_dequantize_{t}")
+                call(fn(R, C_, SA, -(-C_ // 2), SB, -(-C_ // 32), C + off, C_ + off, None))
     assert known == reached, sorted(k.decode() for k in known - reached)
 
 
