@@ -6,7 +6,8 @@
  * for sgemm_f32_ex, this followed by a fused epilogue; gemm_bf16_f32 and
  * gemm_f16_f32 take A and B in 16-bit formats; the MXFP4 entry points, whose
  * operands are 4-bit elements in scaled blocks and whose B is stored by its
- * columns, are described where they begin):
+ * columns, and those of 8-bit integers and of the gated feed-forward block, are
+ * described where they begin):
  *
  *     C[i,j] = sum_{k=0}^{K-1} A[i,k] * B[k,j]      0 <= i < M, 0 <= j < N
  *
@@ -79,11 +80,17 @@ extern "C" {
 #define SGEMM_EALIAS        -4  /* C's address range overlaps A's, B's or bias's */
 #define SGEMM_EHIP          -5  /* the HIP runtime reported an error on launch  */
 #define SGEMM_EINVAL_PATH   -6  /* unknown path selector                        */
-#define SGEMM_EINVAL_ACT    -7  /* unknown activation selector (sgemm_f32_ex)   */
+#define SGEMM_EINVAL_ACT    -7  /* unknown activation selector                  */
 
-/* Activation selectors for sgemm_f32_ex. */
+/* Activation selectors: sgemm_f32_ex takes the first two, the gated entry
+   points all of them. */
 #define SGEMM_ACT_NONE        0 /* identity                                     */
 #define SGEMM_ACT_RELU        1 /* x < 0 ? 0 : x  (NaN passes through)          */
+#define SGEMM_ACT_SILU        2 /* x / (1 + exp(-x))                            */
+#define SGEMM_ACT_GELU        3 /* x P(x), P the standard normal distribution's
+                                   integral: x erfc(-x / sqrt 2) / 2            */
+#define SGEMM_ACT_GELU_TANH   4 /* x (1 + tanh(y)) / 2, y = sqrt(2 / pi) (x +
+                                   0.044715 x^3)                                */
 
 /* Path selectors for sgemm_f32_path. */
 #define SGEMM_PATH_AUTO       0 /* what sgemm_f32 uses: the matrix-core path;
@@ -172,8 +179,8 @@ SGEMM_API const char *sgemm_valu_tile_name(int tile);
  * - K == 0: C = act(beta * C + bias) (the sum is the empty sum, 0).
  * - alpha == 1, beta == 0, bias == NULL, act == SGEMM_ACT_NONE runs exactly
  *   the kernel sgemm_f32 runs, the skinny-shape kernels included.
- * Other arguments, conventions and return codes as sgemm_f32; an act outside
- * SGEMM_ACT_* -> SGEMM_EINVAL_ACT.
+ * Other arguments, conventions and return codes as sgemm_f32; an act other
+ * than SGEMM_ACT_NONE and SGEMM_ACT_RELU -> SGEMM_EINVAL_ACT.
  */
 SGEMM_API int sgemm_f32_ex(int M, int N, int K,
                  const float *A, int lda,
@@ -333,6 +340,124 @@ SGEMM_API int gemm_f16_mxfp4_f32(int M, int N, int K,
                        const void *A, int lda,
                        const void *B, int ldb, const void *SB, int ldsb,
                        float *C, int ldc, void *stream);
+
+/*
+ * 8-bit integers with a scale per row, and the products of a feed-forward
+ * layer.
+ *
+ * A quantised matrix of R rows and K columns is R x K bytes Q, signed whole
+ * numbers at Q + r*ldq (ldq in bytes), and R floats S, contiguous: element (r,c)
+ * stands for Q[r,c] * S[r].  Activations carry one scale per token, weights
+ * (outputs x inputs, used as they are stored) one per output channel.
+ *
+ * Common to these entry points: device pointers, stream order, validation
+ * before any HIP call and the return codes are as above (SGEMM_EALIAS also for
+ * an output that overlaps an input or another output).  Pointers of 16- and
+ * 32-bit data are aligned to their elements, otherwise pointers and leading
+ * dimensions are free; rows that are 16-byte aligned (base and ld) take the fast
+ * loaders.  What lies past a row's length is never written and never matters;
+ * an input row on 16-byte boundaries may be read to the end of its last 16
+ * bytes.  Nothing is allocated, no workspace is used, and every result is the
+ * same from call to call.
+ */
+
+/*
+ * Quantise X (R x C, row-major, ldx in elements) along its rows.  For a row
+ * whose largest magnitude is t: S = max(t / 127 rounded to float, 2^-126), and
+ * each value x becomes the whole number nearest to x / S, ties to the even one
+ * (the quotient is not rounded before).  A row that holds a NaN or an infinity
+ * gets the scale NaN and zeros.  _f32 takes float, _bf16 and _f16 raw 16-bit
+ * storage.
+ */
+SGEMM_API int gemm_i8_quantize_f32(int R, int C, const void *X, int ldx, void *Q, int ldq,
+                         float *S, void *stream);
+SGEMM_API int gemm_i8_quantize_bf16(int R, int C, const void *X, int ldx, void *Q, int ldq,
+                          float *S, void *stream);
+SGEMM_API int gemm_i8_quantize_f16(int R, int C, const void *X, int ldx, void *Q, int ldq,
+                         float *S, void *stream);
+
+/*
+ * Y (R x C, row-major, ldy in elements) = Q[r,c] * S[r], multiplied in fp32 and
+ * rounded to Y's type.
+ */
+SGEMM_API int gemm_i8_dequantize_f32(int R, int C, const void *Q, int ldq, const float *S,
+                           void *Y, int ldy, void *stream);
+SGEMM_API int gemm_i8_dequantize_bf16(int R, int C, const void *Q, int ldq, const float *S,
+                            void *Y, int ldy, void *stream);
+SGEMM_API int gemm_i8_dequantize_f16(int R, int C, const void *Q, int ldq, const float *S,
+                           void *Y, int ldy, void *stream);
+
+/*
+ * C[i,j] = (sum_k A[i,k] * B[j,k]) * SA[i] * SB[j], A (M x K) and B (N x K)
+ * signed bytes, -128 included: the sum is exact in 32-bit integers, then
+ * converted to fp32, multiplied by SA[i], by SB[j], and rounded to C's type (ldc
+ * in elements).  K above 131071, where a sum could pass 32 bits ->
+ * SGEMM_EINVAL_DIM.  K == 0 stores zeros; A, B, SA and SB may then be NULL.
+ */
+SGEMM_API int gemm_i8_f32(int M, int N, int K, const void *A, int lda, const float *SA,
+                const void *B, int ldb, const float *SB, float *C, int ldc, void *stream);
+SGEMM_API int gemm_i8_bf16(int M, int N, int K, const void *A, int lda, const float *SA,
+                 const void *B, int ldb, const float *SB, void *C, int ldc, void *stream);
+SGEMM_API int gemm_i8_f16(int M, int N, int K, const void *A, int lda, const float *SA,
+                const void *B, int ldb, const float *SB, void *C, int ldc, void *stream);
+
+/*
+ * The gated block of a feed-forward layer on 8-bit operands, in one launch:
+ *     H[i,j] = act(g) * u,  g = A.BG^T and u = A.BU^T as gemm_i8_f32 has them,
+ * BG and BU (N x K) the gate's and the other projection's weights.  act is one
+ * of SGEMM_ACT_*; H (M x N) is rounded once.
+ */
+SGEMM_API int gemm_i8_gated_bf16(int M, int N, int K, const void *A, int lda, const float *SA,
+                       const void *BG, int ldbg, const float *SBG,
+                       const void *BU, int ldbu, const float *SBU,
+                       void *H, int ldh, int act, void *stream);
+SGEMM_API int gemm_i8_gated_f16(int M, int N, int K, const void *A, int lda, const float *SA,
+                      const void *BG, int ldbg, const float *SBG,
+                      const void *BU, int ldbu, const float *SBU,
+                      void *H, int ldh, int act, void *stream);
+
+/*
+ * The gated block in 16 bits, in one launch:
+ *     H[i,j] = act(g) * u,  g = sum_k X[i,k] * WG[j,k],  u = sum_k X[i,k] * WU[j,k]
+ * with X (M x K: tokens), WG and WU (N x K: outputs x inputs, as they are
+ * stored), all matrices of one 16-bit type, leading dimensions in elements.
+ * Sums, act and the product are fp32; H is rounded once.  G and U, both or
+ * neither NULL, receive g and u rounded to 16 bits, for the backward pass.
+ * K == 0 stores zeros.
+ */
+SGEMM_API int gemm_gated_bf16(int M, int N, int K, const void *X, int ldx,
+                    const void *WG, int ldwg, const void *WU, int ldwu,
+                    void *G, int ldg, void *U, int ldu, void *H, int ldh, int act, void *stream);
+SGEMM_API int gemm_gated_f16(int M, int N, int K, const void *X, int ldx,
+                   const void *WG, int ldwg, const void *WU, int ldwu,
+                   void *G, int ldg, void *U, int ldu, void *H, int ldh, int act, void *stream);
+
+/*
+ * Its backward pass, from DH (M x N) and what the forward pass kept in G and U:
+ *     DG = DH * U * act'(G)      DU = DH * act(G)                (M x N)
+ *     DX = DG.WG + DU.WU                                         (M x K)
+ *     DWG = DG^T.X               DWU = DU^T.X                    (N x K)
+ * all of one 16-bit type, sums and act in fp32.  Each result is rounded once;
+ * DX, DWG and DWU are products of DG and DU as rounded.  ReLU's slope at 0 is 0.
+ * - DX may be NULL, then it is not computed, and WG, WU and the three leading
+ *   dimensions are not looked at; DWG and DWU may both be NULL, then they are
+ *   not computed and neither they nor X are looked at (one of the two ->
+ *   SGEMM_EINVAL_PTR).  Results overwrite.
+ * - M == 0 sets DWG and DWU to zero, N == 0 sets DX to zero.
+ * Up to three launches, in stream order.
+ */
+SGEMM_API int gemm_gated_backward_bf16(int M, int N, int K, const void *X, int ldx,
+                             const void *WG, int ldwg, const void *WU, int ldwu,
+                             const void *G, int ldg, const void *U, int ldu,
+                             const void *DH, int lddh, void *DG, int lddg, void *DU, int lddu,
+                             void *DX, int lddx, void *DWG, int lddwg, void *DWU, int lddwu,
+                             int act, void *stream);
+SGEMM_API int gemm_gated_backward_f16(int M, int N, int K, const void *X, int ldx,
+                            const void *WG, int ldwg, const void *WU, int ldwu,
+                            const void *G, int ldg, const void *U, int ldu,
+                            const void *DH, int lddh, void *DG, int lddg, void *DU, int lddu,
+                            void *DX, int lddx, void *DWG, int lddwg, void *DWU, int lddwu,
+                            int act, void *stream);
 
 /*
  * The micro-GEMM of "Micro Kernel 입문하기" (teach-meaning.tistory.com/1544),

@@ -13,4 +13,8 @@ from .binding import (  # noqa: F401
     gemm_bf16_mxfp4_f32, gemm_f16_mxfp4_f32, gemm_mxfp4_bf16, gemm_mxfp4_dequantize_bf16,
     gemm_mxfp4_dequantize_f16, gemm_mxfp4_dequantize_f32, gemm_mxfp4_f32,
     gemm_mxfp4_quantize_bf16, gemm_mxfp4_quantize_f16, gemm_mxfp4_quantize_f32,
+    gemm_gated_backward_bf16, gemm_gated_backward_f16, gemm_gated_bf16, gemm_gated_f16,
+    gemm_i8_bf16, gemm_i8_dequantize_bf16, gemm_i8_dequantize_f16, gemm_i8_dequantize_f32,
+    gemm_i8_f16, gemm_i8_f32, gemm_i8_gated_bf16, gemm_i8_gated_f16, gemm_i8_quantize_bf16,
+    gemm_i8_quantize_f16, gemm_i8_quantize_f32,
 )

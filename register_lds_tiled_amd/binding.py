@@ -30,6 +30,11 @@ SGEMM_EINVAL_ACT = -7
 ACT_NONE = 0
 ACT_RELU = 1
 ACTS = {"none": ACT_NONE, "relu": ACT_RELU}
+# the gated entry points' activations
+ACT_SILU = 2
+ACT_GELU = 3
+ACT_GELU_TANH = 4
+GATED_ACTS = {**ACTS, "silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
 
 PATH_AUTO = 0
 PATH_VALU = 1
@@ -43,7 +48,12 @@ EXPORTS = ("sgemm_f32", "sgemm_f32_path", "sgemm_f32_ex", "gemm_bf16_f32", "gemm
            "sgemm_abi_version", "gemm_mxfp4_quantize_f32", "gemm_mxfp4_quantize_bf16",
            "gemm_mxfp4_quantize_f16", "gemm_mxfp4_dequantize_f32", "gemm_mxfp4_dequantize_bf16",
            "gemm_mxfp4_dequantize_f16", "gemm_mxfp4_f32", "gemm_mxfp4_bf16",
-           "gemm_bf16_mxfp4_f32", "gemm_f16_mxfp4_f32")
+           "gemm_bf16_mxfp4_f32", "gemm_f16_mxfp4_f32",
+           "gemm_i8_quantize_f32", "gemm_i8_quantize_bf16", "gemm_i8_quantize_f16",
+           "gemm_i8_dequantize_f32", "gemm_i8_dequantize_bf16", "gemm_i8_dequantize_f16",
+           "gemm_i8_f32", "gemm_i8_bf16", "gemm_i8_f16", "gemm_i8_gated_bf16",
+           "gemm_i8_gated_f16", "gemm_gated_bf16", "gemm_gated_f16",
+           "gemm_gated_backward_bf16", "gemm_gated_backward_f16")
 
 _lib = None
 _lib_poison = None
@@ -95,6 +105,20 @@ def _load(path: str):
         fn.argtypes, fn.restype = [i, i, i, p, i, p, i, p, i, p, i, p, i, p], i
     for fn in (lib.gemm_bf16_mxfp4_f32, lib.gemm_f16_mxfp4_f32):
         fn.argtypes, fn.restype = [i, i, i, p, i, p, i, p, i, p, i, p], i
+    for t in ("f32", "bf16", "f16"):
+        fn = getattr(lib, f"gemm_i8_quantize_{t}")
+        fn.argtypes, fn.restype = [i, i, p, i, p, i, p, p], i
+        fn = getattr(lib, f"gemm_i8_dequantize_{t}")
+        fn.argtypes, fn.restype = [i, i, p, i, p, p, i, p], i
+        fn = getattr(lib, f"gemm_i8_{t}")
+        fn.argtypes, fn.restype = [i, i, i, p, i, p, p, i, p, p, i, p], i
+    for t in ("bf16", "f16"):
+        fn = getattr(lib, f"gemm_i8_gated_{t}")
+        fn.argtypes, fn.restype = [i, i, i] + [p, i, p] * 3 + [p, i, i, p], i
+        fn = getattr(lib, f"gemm_gated_{t}")
+        fn.argtypes, fn.restype = [i, i, i] + [p, i] * 6 + [i, p], i
+        fn = getattr(lib, f"gemm_gated_backward_{t}")
+        fn.argtypes, fn.restype = [i, i, i] + [p, i] * 11 + [i, p], i
     lib.sgemm_status_string.argtypes = [i]
     lib.sgemm_status_string.restype = ctypes.c_char_p
     lib.sgemm_last_error.argtypes = []
@@ -270,7 +294,8 @@ def _mx_kinds():
         _MX_KINDS = {"f32": {torch.float32}, "bf16": {torch.bfloat16} | raw16,
                      "f16": {torch.float16} | raw16,
                      "codes": {torch.uint8} | extra("float4_e2m1fn_x2"),
-                     "scales": {torch.uint8} | extra("float8_e8m0fnu")}
+                     "scales": {torch.uint8} | extra("float8_e8m0fnu"),
+                     "i8": {torch.int8}, "vector": {torch.float32}}
     return _MX_KINDS
 
 
@@ -293,11 +318,13 @@ def _no_c_int(name, n):
     raise OverflowError(f"{name}: {n} does not fit the library's int")
 
 
-def _mx_call(name, head, operands, stream, check):
-    """One MXFP4 entry point: `head` its leading integers, `operands` (kind,
-    address or tensor or None, leading dimension) in the C order, all of them
-    within a C int's range.  Tensors lie on one device, whose current stream is
-    the default and which is the current device during the call."""
+def _mx_call(name, head, operands, stream, check, tail=()):
+    """One entry point of the MXFP4, 8-bit integer and gated families: `head` its
+    leading integers, `operands` (kind, address or tensor or None, leading
+    dimension; "vector" has none) in the C order, `tail` the integers behind
+    them, all of them within a C int's range.  Tensors lie on one device, whose
+    current stream is the default and which is the current device during the
+    call."""
     if _torch is None:
         _mx_setup()
     tensor = _torch.Tensor
@@ -322,7 +349,12 @@ def _mx_call(name, head, operands, stream, check):
         elif x is not None:
             x = _ptr(x)
         args.append(x)
-        args.append(ld)
+        if kind != "vector":
+            args.append(ld)
+    for n in tail:
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
+            _no_c_int(name, n)
+        args.append(n)
     fn = getattr(_lib or library(), name)
     if dev is not None and dev != _torch.cuda.current_device():
         with _torch.cuda.device(dev):
@@ -407,6 +439,151 @@ def gemm_f16_mxfp4_f32(M, N, K, A, lda, B, ldb, SB, ldsb, C, ldc, stream=None, *
     return _mx_call("gemm_f16_mxfp4_f32", (M, N, K),
                     (("f16", A, lda), ("codes", B, ldb), ("scales", SB, ldsb), ("f32", C, ldc)),
                     stream, check)
+
+
+# ---- 8-bit integers with a scale per row, and the gated feed-forward block --
+
+def _vector(name, x, n):
+    """A scales operand: a tensor of `n` neighbouring floats, or an address."""
+    if hasattr(x, "numel") and (x.numel() < n or not x.is_contiguous()):
+        raise ValueError(f"{name}: {n} scales are {n} neighbouring floats")
+    return "vector", x, 0
+
+
+def _act(act):
+    return GATED_ACTS[act] if isinstance(act, str) else int(act)
+
+
+def _i8_quantize(t, R, C, X, ldx, Q, ldq, S, stream, check):
+    name = f"gemm_i8_quantize_{t}"
+    return _mx_call(name, (R, C), ((t, X, ldx), ("i8", Q, ldq), _vector(name, S, R)), stream, check)
+
+
+def gemm_i8_quantize_f32(R, C, X, ldx, Q, ldq, S, stream=None, *, check=True) -> int:
+    """X (R x C, float32) to whole numbers Q (int8) with a scale per row S (R
+    neighbouring float32): X is Q * S[:, None], each off by half a scale at most."""
+    return _i8_quantize("f32", R, C, X, ldx, Q, ldq, S, stream, check)
+
+
+def gemm_i8_quantize_bf16(R, C, X, ldx, Q, ldq, S, stream=None, *, check=True) -> int:
+    """gemm_i8_quantize_f32 for bfloat16 X."""
+    return _i8_quantize("bf16", R, C, X, ldx, Q, ldq, S, stream, check)
+
+
+def gemm_i8_quantize_f16(R, C, X, ldx, Q, ldq, S, stream=None, *, check=True) -> int:
+    """gemm_i8_quantize_f32 for binary16 X."""
+    return _i8_quantize("f16", R, C, X, ldx, Q, ldq, S, stream, check)
+
+
+def _i8_dequantize(t, R, C, Q, ldq, S, Y, ldy, stream, check):
+    name = f"gemm_i8_dequantize_{t}"
+    return _mx_call(name, (R, C), (("i8", Q, ldq), _vector(name, S, R), (t, Y, ldy)), stream, check)
+
+
+def gemm_i8_dequantize_f32(R, C, Q, ldq, S, Y, ldy, stream=None, *, check=True) -> int:
+    """Y (R x C, float32) = Q * S[:, None]."""
+    return _i8_dequantize("f32", R, C, Q, ldq, S, Y, ldy, stream, check)
+
+
+def gemm_i8_dequantize_bf16(R, C, Q, ldq, S, Y, ldy, stream=None, *, check=True) -> int:
+    """gemm_i8_dequantize_f32 into bfloat16 Y."""
+    return _i8_dequantize("bf16", R, C, Q, ldq, S, Y, ldy, stream, check)
+
+
+def gemm_i8_dequantize_f16(R, C, Q, ldq, S, Y, ldy, stream=None, *, check=True) -> int:
+    """gemm_i8_dequantize_f32 into binary16 Y."""
+    return _i8_dequantize("f16", R, C, Q, ldq, S, Y, ldy, stream, check)
+
+
+def _i8_product(t, M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check):
+    name = f"gemm_i8_{t}"
+    return _mx_call(name, (M, N, K), (("i8", A, lda), _vector(name, SA, M), ("i8", B, ldb),
+                                      _vector(name, SB, N), (t, C, ldc)), stream, check)
+
+
+def gemm_i8_f32(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream=None, *, check=True) -> int:
+    """C = (A.B^T) * SA[:, None] * SB, A (M x K) and B (N x K) int8, the sums
+    exact, float32 C."""
+    return _i8_product("f32", M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check)
+
+
+def gemm_i8_bf16(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream=None, *, check=True) -> int:
+    """gemm_i8_f32 with C rounded to bfloat16."""
+    return _i8_product("bf16", M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check)
+
+
+def gemm_i8_f16(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream=None, *, check=True) -> int:
+    """gemm_i8_f32 with C rounded to binary16."""
+    return _i8_product("f16", M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check)
+
+
+def _i8_gated(t, M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh, act, stream, check):
+    name = f"gemm_i8_gated_{t}"
+    return _mx_call(name, (M, N, K), (("i8", A, lda), _vector(name, SA, M), ("i8", BG, ldbg),
+                                      _vector(name, SBG, N), ("i8", BU, ldbu),
+                                      _vector(name, SBU, N), (t, H, ldh)), stream, check,
+                    (_act(act),))
+
+
+def gemm_i8_gated_bf16(M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh,
+                       act=ACT_SILU, stream=None, *, check=True) -> int:
+    """H = act(g) * u with g and u the products gemm_i8_f32 makes of A with BG and
+    BU, H (M x N) bfloat16; act is an int or a name in GATED_ACTS."""
+    return _i8_gated("bf16", M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh, act,
+                     stream, check)
+
+
+def gemm_i8_gated_f16(M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh,
+                      act=ACT_SILU, stream=None, *, check=True) -> int:
+    """gemm_i8_gated_bf16 into binary16 H."""
+    return _i8_gated("f16", M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh, act,
+                     stream, check)
+
+
+def _gated(t, M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh, act, stream, check):
+    return _mx_call(f"gemm_gated_{t}", (M, N, K),
+                    ((t, X, ldx), (t, WG, ldwg), (t, WU, ldwu), (t, G, ldg), (t, U, ldu),
+                     (t, H, ldh)), stream, check, (_act(act),))
+
+
+def gemm_gated_bf16(M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh, act=ACT_SILU,
+                    stream=None, *, check=True) -> int:
+    """H = act(X.WG^T) * (X.WU^T), X (M x K), WG and WU (N x K), H (M x N) bfloat16;
+    G and U, both or neither None, receive the two products."""
+    return _gated("bf16", M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh, act,
+                  stream, check)
+
+
+def gemm_gated_f16(M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh, act=ACT_SILU,
+                   stream=None, *, check=True) -> int:
+    """gemm_gated_bf16 in binary16."""
+    return _gated("f16", M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh, act,
+                  stream, check)
+
+
+def _gated_backward(t, M, N, K, operands, act, stream, check):
+    it = iter(operands)
+    return _mx_call(f"gemm_gated_backward_{t}", (M, N, K), [(t, x, ld) for x, ld in zip(it, it)],
+                    stream, check, (_act(act),))
+
+
+def gemm_gated_backward_bf16(M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, DH, lddh,
+                             DG, lddg, DU, lddu, DX, lddx, DWG, lddwg, DWU, lddwu,
+                             act=ACT_SILU, stream=None, *, check=True) -> int:
+    """The gradients of gemm_gated_bf16 from DH: DG and DU (M x N), DX (M x K, or
+    None), DWG and DWU (N x K, or both None)."""
+    return _gated_backward("bf16", M, N, K, (X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, DH, lddh,
+                                             DG, lddg, DU, lddu, DX, lddx, DWG, lddwg, DWU, lddwu),
+                           act, stream, check)
+
+
+def gemm_gated_backward_f16(M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, DH, lddh,
+                            DG, lddg, DU, lddu, DX, lddx, DWG, lddwg, DWU, lddwu,
+                            act=ACT_SILU, stream=None, *, check=True) -> int:
+    """gemm_gated_backward_bf16 in binary16."""
+    return _gated_backward("f16", M, N, K, (X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, DH, lddh,
+                                            DG, lddg, DU, lddu, DX, lddx, DWG, lddwg, DWU, lddwu),
+                           act, stream, check)
 
 
 def matmul(A, B, out=None, path=PATH_AUTO, stream=None):

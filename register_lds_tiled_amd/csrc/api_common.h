@@ -40,6 +40,29 @@ inline Range span(const void* p, long long rows, long long cols, long long ld,
     return {lo, (uintptr_t)hi, true};
 }
 inline bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+inline long long at_least_1(long long n) { return n > 1 ? n : 1; }
+
+// Up to twelve byte ranges, outputs first: every output must keep clear of
+// all others.
+struct Ranges {
+    Range r[12];
+    int n = 0, outputs = 0;
+    bool ok = true;
+    void add(const void* p, long long rows, long long row_elements, long long ld, long long esize,
+             bool output = false) {
+        r[n] = span(p, rows, row_elements, ld, esize);
+        ok = ok && r[n].ok;
+        ++n;
+        if (output) outputs = n;
+    }
+    int status() const {
+        if (!ok) return SGEMM_EINVAL_DIM;
+        for (int i = 0; i < outputs; ++i)
+            for (int j = i + 1; j < n; ++j)
+                if (overlaps(r[i], r[j])) return SGEMM_EALIAS;
+        return SGEMM_OK;
+    }
+};
 
 // Compute units and XCDs of the device a stream's launches run on, queried
 // once per device (the first 64 device ids) and then read from the cache.

@@ -1,0 +1,69 @@
+// gated_backward.hip -- the gated block's gradients in 16 bits: dG and dU element
+// by element, dX = dG.Wg + dU.Wu as one product over both, dWg = dG^T.X and
+// dWu = dU^T.X in one launch.
+#include "layer_tile.h"
+
+namespace sgemm {
+namespace {
+
+// A thread takes eight columns down the rows: three reads, two writes, bound by
+// memory.
+template <Elem E>
+__global__ __launch_bounds__(256) void gated_slopes_kernel(GateArgs p, int shift) {
+    const int units = (int)(((long long)p.N + 7) / 8);
+    const long long i = ((long long)blockIdx.x << shift) + (threadIdx.x & ((1 << shift) - 1));
+    if (i >= units) return;
+    const int n = p.N - 8 * (int)i;
+    const long long rows = (long long)gridDim.y << (8 - shift);
+    with_act(p.act, [&](auto act) __attribute__((always_inline)) {
+        for (long long r = ((long long)blockIdx.y << (8 - shift)) + (threadIdx.x >> shift); r < p.M; r += rows) {
+            float g[8], u[8], dh[8], dg[8], du[8];
+            load8<E>(p.G + 2 * r * p.ldg, 8 * i, p.N, g);
+            load8<E>(p.U + 2 * r * p.ldu, 8 * i, p.N, u);
+            load8<E>(p.DH + 2 * r * p.lddh, 8 * i, p.N, dh);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float a, d;
+                act_and_slope<act>(g[e], a, d);
+                dg[e] = dh[e] * u[e] * d;
+                du[e] = dh[e] * a;
+            }
+            typedef type_of<E> O;
+            store8<E>(reinterpret_cast<O*>(p.DG) + r * p.lddg + 8 * i, dg, n);
+            store8<E>(reinterpret_cast<O*>(p.DU) + r * p.lddu + 8 * i, du, n);
+        }
+    });
+}
+
+template <Elem E>
+hipError_t slopes(const GateArgs& a, hipStream_t s) {
+    const long long units = ((long long)a.N + 7) / 8;
+    int shift = 0;
+    while (shift < 8 && (1 << shift) < units) ++shift;
+    const long long gx = (units + (1 << shift) - 1) >> shift, by = ((long long)a.M + (256 >> shift) - 1) >> (8 - shift);
+    long long gy = (64ll * a.cus + gx - 1) / gx;   // rows beyond it go round
+    if (gy > by) gy = by;
+    if (gy > 65535) gy = 65535;
+    gated_slopes_kernel<E><<<dim3((unsigned)gx, (unsigned)gy), 256, 0, s>>>(a, shift);
+    return hipGetLastError();
+}
+
+template <Form F, Elem E>
+hipError_t launch(const LayerArgs& a, hipStream_t s) {
+    using T = layer::Tile<F, E, E, 128, 128, 64, 64>;
+    return layer::launch_tiles<T>(layer::tile_kernel<T>, a, s);
+}
+
+}  // namespace
+
+hipError_t launch_gated_slopes(const GateArgs& a, Elem t, hipStream_t s) {
+    return t == Elem::bf16 ? slopes<Elem::bf16>(a, s) : slopes<Elem::f16>(a, s);
+}
+hipError_t launch_gated_dx(const LayerArgs& a, Elem t, hipStream_t s) {
+    return t == Elem::bf16 ? launch<Form::sum2, Elem::bf16>(a, s) : launch<Form::sum2, Elem::f16>(a, s);
+}
+hipError_t launch_gated_dw(const LayerArgs& a, Elem t, hipStream_t s) {
+    return t == Elem::bf16 ? launch<Form::both, Elem::bf16>(a, s) : launch<Form::both, Elem::f16>(a, s);
+}
+
+}  // namespace sgemm

@@ -1,0 +1,288 @@
+// layer_tile.h -- tile kernels of the feed-forward layer's products on the matrix
+// cores, and the epilogue that they share.
+//
+// One shape serves both element sizes: a matrix instruction of 32 x 32 outputs
+// takes 16 bytes of a row of each operand per lane, 16 k in 16 bits
+// (v_mfma_f32_32x32x16) and 32 in 8 (v_mfma_i32_32x32x32_i8), in the same number
+// of cycles.  A stage is 64 bytes of k (two instructions deep); k terms may come
+// in any order, so step t gives lane half h the 16-byte chunk 2h + t.
+//
+// An operand whose rows run along k lies in LDS as rows of four chunks, chunk c
+// of row r at c ^ chunk_at(r).  LDS serves a 16-byte read 16 lanes at a time,
+// lanes 0-3, 12-15, 20-23, 24-27 together and lanes 4-11, 16-19, 28-31 together:
+// of such rows four share a 64-byte place of the 256-byte window of banks, and
+// their chunk_at differ.
+//
+// An operand of 16-bit elements whose rows run across k lies as 32 k rows of W
+// columns, chunk c of row k at c ^ 4 (k % 4), and comes out of LDS through the
+// transposing read: within 16 lanes, element e of lane i is element i % 4 of the
+// 8 bytes that lane 4e + i / 4 addresses.
+//
+// The gated form multiplies two matrices by the same rows of A: of a wave's
+// columns the first half are rows of the first matrix, the second half the same
+// rows of the second, so that both products of an output are in one lane.
+#pragma once
+
+#include "layer.h"
+
+namespace sgemm {
+#ifdef __HIPCC__
+namespace layer {
+
+__device__ __forceinline__ int chunk_at(int r) { return r >> 3 & 3; }
+
+template <Elem E>
+using acc_of = std::conditional_t<E == Elem::i8, intx16, floatx16>;
+
+template <Elem E>
+__device__ __forceinline__ acc_of<E> mfma(uint4 a, uint4 b, acc_of<E> c) {
+    if constexpr (E == Elem::i8)
+        return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(intx4, a), __builtin_bit_cast(intx4, b), c, 0,
+                                                     0, 0);
+    else if constexpr (E == Elem::bf16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0,
+                                                       0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0,
+                                                      0, 0);
+}
+
+template <Form F, Elem E_, Elem OUT_, int BM_, int BN_, int WM_, int WN_, int GROUP_M_ = 8>
+struct Tile {
+    static constexpr Form FORM = F;
+    static constexpr Elem E = E_, OUT = OUT_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GROUP_M = GROUP_M_;
+    static constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N, NT = 64 * NW;
+    static constexpr int FM = WM / 32, FN = WN / 32;
+    static constexpr bool GATED = F == Form::gated;
+    static constexpr bool A_ACROSS = F == Form::both, B_ACROSS = F == Form::sum2 || F == Form::both;
+    static constexpr int ES = size_of<E>, KST = 64 / ES;          // k of a stage
+    static constexpr int SA = BM * 64, SB = BN * 64;              // bytes of a stage
+    static constexpr int COLS = GATED ? BN / 2 : BN;              // columns of C
+    static constexpr int PAIRS = F == Form::sum2 ? 2 : 1;
+    static constexpr int OUTS = F == Form::both ? 2 : 1;
+    // the epilogue's rows: 32 of WN values, rows four apart in the other half of the banks
+    static constexpr int STR = WN + 8;
+    static constexpr int EPI = NW * 32 * STR * 4;                 // bytes
+    static_assert(4 * STR % 64 == 32, "rows four apart");
+    static_assert(!GATED || WN % 64 == 0, "two halves of whole blocks");
+};
+
+// A wave's outputs from its accumulators: 32 rows at a time through LDS (mine:
+// 32 STR words of the wave's own), so that a lane has eight neighbouring columns
+// and stores them whole.  r0, c0: the first row and column of C.
+template <class T, class Acc>
+__device__ __forceinline__ void epilogue(const LayerArgs& p, int out, const Acc (&acc)[T::FM][T::FN], float* mine,
+                                         long long r0, long long c0, int lane) {
+    constexpr int WCOLS = T::GATED ? T::WN / 2 : T::WN;   // columns of C in a wave
+    constexpr int UNITS = WCOLS / 8;
+    const int li = lane & 31, g = lane >> 5;
+    const long long cols = p.N - c0;
+    typedef type_of<T::OUT> O;
+    O* const C = static_cast<O*>(p.C[out]);
+    static_for<T::FM>([&](auto i) __attribute__((always_inline)) {
+        lane_order();
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const auto v = acc[i][j][r];   // (a bit cast of the element itself would take the vector's first)
+                mine[(8 * (r / 4) + 4 * g + r % 4) * T::STR + 32 * j + li] = __builtin_bit_cast(float, v);
+            }
+        lane_order();
+#pragma unroll 1
+        for (int id = lane; id < 32 * UNITS; id += 64) {
+            const int row = id / UNITS, u = id % UNITS;
+            const long long R = r0 + 32 * i + row;
+            const int n = (int)min(cols - 8 * u, 8ll);
+            if (R >= p.M || n <= 0) continue;
+            float x[8], y[8];
+            const float* const from = mine + row * T::STR + 8 * u;
+            __builtin_memcpy(x, from, 32);
+            if constexpr (T::GATED) __builtin_memcpy(y, from + WCOLS, 32);
+            if constexpr (T::E == Elem::i8) {
+                const float sa = p.K > 0 ? p.SA[R] : 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const long long c = c0 + 8 * u + min(e, n - 1);
+                    x[e] = (float)__float_as_int(x[e]) * sa * (p.K > 0 ? p.SB[0][c] : 0.f);
+                    if constexpr (T::GATED) y[e] = (float)__float_as_int(y[e]) * sa * (p.K > 0 ? p.SB[1][c] : 0.f);
+                }
+            }
+            const long long at = c0 + 8 * u;
+            if constexpr (T::GATED) {
+                if constexpr (T::E != Elem::i8)
+                    if (p.G != nullptr) {
+                        store8<T::OUT>(static_cast<O*>(p.G) + R * p.ldg + at, x, n);
+                        store8<T::OUT>(static_cast<O*>(p.U) + R * p.ldu + at, y, n);
+                    }
+                with_act(p.act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = act_of<a>(x[e]) * y[e];
+                });
+            }
+            store8<T::OUT>(C + R * p.ldc[out] + at, x, n);
+        }
+    });
+}
+
+// Where a wave's operand lies in a stage: byte offsets of step t's read of block
+// j (32 rows or columns from w on).
+__device__ __forceinline__ int along_at(int w, int j, int t, int li, int g) {
+    return (w + 32 * j + li) * 64 + 16 * ((2 * g + t) ^ chunk_at(li));
+}
+// The lower read of two (k .. k + 3 of the lane's eight); the upper is 4 rows on.
+template <int W>
+__device__ __forceinline__ int across_at(int w, int j, int t, int lane) {
+    const int q = lane >> 4, e = (lane >> 2) & 3, n = lane & 3;
+    const int k = 16 * (q >> 1) + e + 8 * t, col = w + 32 * j + 16 * (q & 1) + 4 * n;
+    return 2 * (k * W + (((col >> 3) ^ (4 * e)) << 3 | (col & 7)));
+}
+template <int W>
+__device__ __forceinline__ uint4 read_across(const unsigned char* at) {
+    const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_shortx4*)(__attribute__((address_space(3))) const unsigned char*)at);
+    const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_shortx4*)(__attribute__((address_space(3))) const unsigned char*)(at + 8 * W));
+    const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
+    return make_uint4(l.x, l.y, h.x, h.y);
+}
+
+// Row r of B's tile in the gated form: which matrix, and which row from the
+// tile's first on.
+template <class T>
+__device__ __forceinline__ void gated_row(int r, int& m, int& row) {
+    constexpr int H = T::WN / 2;
+    m = r / H & 1;
+    row = r / T::WN * H + r % H;
+}
+
+// Tiles through registers: any alignment, pitch and length.  Two LDS stages, one
+// barrier a stage: the next stage is loaded while one multiplies, and written to
+// the other place behind it.
+template <class T>
+__global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m, int tiles_n) {
+    constexpr int BM = T::BM, BN = T::BN, NT = T::NT, FM = T::FM, FN = T::FN, KST = T::KST;
+    constexpr int CA = BM * 4 / NT, CB = BN * 4 / NT;             // a thread's chunks
+    static_assert(CA * NT == BM * 4 && CB * NT == BN * 4, "whole rounds of the loader");
+    constexpr int STAGE = T::SA + T::SB, ROOM = 2 * STAGE > T::EPI ? 2 * STAGE : T::EPI;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[ROOM];
+    const int per = tiles_m * tiles_n;
+    const int out = T::OUTS == 2 ? blockIdx.x / per : 0;
+    int tm, tn;
+    tile_coords(blockIdx.x - out * per, tiles_m, tiles_n, T::GROUP_M, p.xcds, tm, tn);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = (wave / T::WAVES_N) * T::WM, wn = (wave % T::WAVES_N) * T::WN;
+    const int li = lane & 31, g = lane >> 5;
+    const long long m0 = (long long)tm * BM, n0 = (long long)tn * T::COLS;
+    const long long row_bytes = (long long)p.K * T::ES;
+    const long long each = ((long long)p.K + KST - 1) / KST, stages = each * T::PAIRS;
+
+    // A chunk of an operand whose rows run along k (row of its matrix), or
+    // across it (k row, and the byte of its first column).
+    auto along = [&](const unsigned char* M, long long ld, long long row, long long s, int c) {
+        return mx_bytes16(M + row * ld, s * 64 + 16 * c, row_bytes);
+    };
+    auto across = [&](const unsigned char* M, long long ld, long long k, long long at, long long len) {
+        return k < p.K ? mx_bytes16(M + k * ld, at, len) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 va[CA], vb[CB];
+    auto fetch = [&](long long s) __attribute__((always_inline)) {
+        const int pair = T::PAIRS == 2 && s >= each ? 1 : 0;
+        const long long st = s - pair * each;
+        const int ma = T::OUTS == 2 ? out : pair;
+#pragma unroll
+        for (int u = 0; u < CA; ++u) {
+            const int id = tid + u * NT;
+            if constexpr (T::A_ACROSS)
+                va[u] = across(p.A[ma], p.lda[ma], st * KST + id / (BM / 8), 2 * m0 + 16 * (id % (BM / 8)), 2ll * p.M);
+            else
+                va[u] = along(p.A[ma], p.lda[ma], min(m0 + (id >> 2), (long long)p.M - 1), st, id & 3);
+        }
+#pragma unroll
+        for (int u = 0; u < CB; ++u) {
+            const int id = tid + u * NT;
+            if constexpr (T::B_ACROSS) {
+                vb[u] = across(p.B[pair], p.ldb[pair], st * KST + id / (BN / 8), 2 * n0 + 16 * (id % (BN / 8)), 2ll * p.N);
+            } else {
+                int m = 0, row = id >> 2;
+                if constexpr (T::GATED) gated_row<T>(id >> 2, m, row);
+                vb[u] = along(m ? p.B[1] : p.B[0], m ? p.ldb[1] : p.ldb[0], min(n0 + row, (long long)p.N - 1), st, id & 3);
+            }
+        }
+    };
+    auto place = [&](int buf) __attribute__((always_inline)) {
+        unsigned char* const to = lds + buf * STAGE;
+        auto put = [](unsigned char* at, uint4 v) {
+            lds_poison_f4(at);
+            *reinterpret_cast<uint4*>(at) = v;
+        };
+#pragma unroll
+        for (int u = 0; u < CA; ++u) {
+            const int id = tid + u * NT;
+            if constexpr (T::A_ACROSS)
+                put(to + id / (BM / 8) * (2 * BM) + 16 * (id % (BM / 8) ^ 4 * (id / (BM / 8) & 3)), va[u]);
+            else
+                put(to + (id >> 2) * 64 + 16 * ((id & 3) ^ chunk_at(id >> 2)), va[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < CB; ++u) {
+            const int id = tid + u * NT;
+            if constexpr (T::B_ACROSS)
+                put(to + T::SA + id / (BN / 8) * (2 * BN) + 16 * (id % (BN / 8) ^ 4 * (id / (BN / 8) & 3)), vb[u]);
+            else
+                put(to + T::SA + (id >> 2) * 64 + 16 * ((id & 3) ^ chunk_at(id >> 2)), vb[u]);
+        }
+    };
+
+    acc_of<T::E> acc[FM][FN] = {};
+    if (stages > 0) {
+        fetch(0);
+        place(0);
+    }
+    __syncthreads();
+    for (long long s = 0; s < stages; ++s) {
+        if (s + 1 < stages) fetch(s + 1);
+        const unsigned char* const st = lds + (s & 1) * STAGE;
+        static_for<2>([&](auto t) __attribute__((always_inline)) {
+            uint4 a[FM], b[FN];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                if constexpr (T::A_ACROSS)
+                    a[i] = read_across<BM>(st + across_at<BM>(wm, i, t, lane));
+                else
+                    a[i] = *reinterpret_cast<const uint4*>(st + along_at(wm, i, t, li, g));
+            }
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                if constexpr (T::B_ACROSS)
+                    b[j] = read_across<BN>(st + T::SA + across_at<BN>(wn, j, t, lane));
+                else
+                    b[j] = *reinterpret_cast<const uint4*>(st + T::SA + along_at(wn, j, t, li, g));
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = mfma<T::E>(a[i], b[j], acc[i][j]);
+        });
+        if (s + 1 < stages) place((int)((s + 1) & 1));
+        __syncthreads();
+    }
+    epilogue<T>(p, out, acc, reinterpret_cast<float*>(lds) + wave * 32 * T::STR, m0 + wm,
+                n0 + (T::GATED ? wn / 2 : wn), lane);
+}
+
+// One workgroup per tile; more threads than a launch holds are refused by the
+// argument checks.
+template <class T, class K>
+hipError_t launch_tiles(K kernel, const LayerArgs& a, hipStream_t s) {
+    const long long tm = ((long long)a.M + T::BM - 1) / T::BM, tn = ((long long)a.N + T::COLS - 1) / T::COLS;
+    if (tm * tn * T::OUTS * T::NT > 0xFFFFFFFFll) return hipErrorInvalidValue;
+    kernel<<<(unsigned)(tm * tn * T::OUTS), T::NT, 0, s>>>(a, (int)tm, (int)tn);
+    return hipGetLastError();
+}
+
+}  // namespace layer
+#endif
+}  // namespace sgemm

@@ -10,29 +10,6 @@ using namespace sgemm;
 
 long long value_bytes(int k) { return ((long long)k + 1) / 2; }
 long long scale_bytes(int k) { return ((long long)k + 31) / 32; }
-long long at_least_1(long long n) { return n > 1 ? n : 1; }
-
-// Up to eight byte ranges, outputs first: every output must keep clear of
-// all others.
-struct Ranges {
-    Range r[8];
-    int n = 0, outputs = 0;
-    bool ok = true;
-    void add(const void* p, long long rows, long long row_elements, long long ld, long long esize,
-             bool output = false) {
-        r[n] = span(p, rows, row_elements, ld, esize);
-        ok = ok && r[n].ok;
-        ++n;
-        if (output) outputs = n;
-    }
-    int status() const {
-        if (!ok) return SGEMM_EINVAL_DIM;
-        for (int i = 0; i < outputs; ++i)
-            for (int j = i + 1; j < n; ++j)
-                if (overlaps(r[i], r[j])) return SGEMM_EALIAS;
-        return SGEMM_OK;
-    }
-};
 
 int quantize(int R, int C, const void* X, int ldx, void* Q, int ldq, void* S, int lds, void* QT,
              int ldqt, void* ST, int ldst, void* stream, MxType t) {
