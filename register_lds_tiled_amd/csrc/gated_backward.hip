@@ -1,7 +1,7 @@
 // gated_backward.hip -- the gated block's gradients in 16 bits: dG and dU element
 // by element, dX = dG.Wg + dU.Wu as one product over both, dWg = dG^T.X and
 // dWu = dU^T.X in one launch.
-#include "layer_tile.h"
+#include "layer_big.h"
 
 namespace sgemm {
 namespace {
@@ -50,8 +50,7 @@ hipError_t slopes(const GateArgs& a, hipStream_t s) {
 
 template <Form F, Elem E>
 hipError_t launch(const LayerArgs& a, hipStream_t s) {
-    using T = layer::Tile<F, E, E, 128, 128, 64, 64>;
-    return layer::launch_tiles<T>(layer::tile_kernel<T>, a, s);
+    return layer::launch_form<F, E, E>(a, s);
 }
 
 }  // namespace

@@ -1,14 +1,13 @@
 // i8_gemm.hip -- C = A.B^T of 8-bit whole numbers, summed in 32 bits and scaled by
 // token and channel, and the gated block on such operands.
-#include "layer_tile.h"
+#include "layer_big.h"
 
 namespace sgemm {
 namespace {
 
 template <Form F, Elem OUT>
 hipError_t launch(const LayerArgs& a, hipStream_t s) {
-    using T = layer::Tile<F, Elem::i8, OUT, 128, 128, 64, 64>;
-    return layer::launch_tiles<T>(layer::tile_kernel<T>, a, s);
+    return layer::launch_form<F, Elem::i8, OUT>(a, s);
 }
 
 }  // namespace

@@ -168,7 +168,7 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
     constexpr int STAGE = T::SA + T::SB, ROOM = 2 * STAGE > T::EPI ? 2 * STAGE : T::EPI;
     __shared__ __attribute__((aligned(16))) unsigned char lds[ROOM];
     const int per = tiles_m * tiles_n;
-    const int out = T::OUTS == 2 ? blockIdx.x / per : 0;
+    const int out = T::OUTS == 2 && (int)blockIdx.x >= per ? 1 : 0;
     int tm, tn;
     tile_coords(blockIdx.x - out * per, tiles_m, tiles_n, T::GROUP_M, p.xcds, tm, tn);
     const int tid = threadIdx.x, lane = tid & 63;
