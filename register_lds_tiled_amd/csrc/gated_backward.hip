@@ -1,7 +1,7 @@
 // gated_backward.hip -- the gated block's gradients in 16 bits: dG and dU element
 // by element, dX = dG.Wg + dU.Wu as one product over both, dWg = dG^T.X and
 // dWu = dU^T.X in one launch.
-#include "layer_big.h"
+#include "layer_split.h"
 
 namespace sgemm {
 namespace {

@@ -1,23 +1,15 @@
 // i8_gemm.hip -- C = A.B^T of 8-bit whole numbers, summed in 32 bits and scaled by
-// token and channel, and the gated block on such operands.
-#include "layer_big.h"
+// token and channel.
+#include "layer_rows.h"
+#include "layer_split.h"
 
 namespace sgemm {
-namespace {
-
-template <Form F, Elem OUT>
-hipError_t launch(const LayerArgs& a, hipStream_t s) {
-    return layer::launch_form<F, Elem::i8, OUT>(a, s);
-}
-
-}  // namespace
 
 hipError_t launch_i8_nt(const LayerArgs& a, Elem out, hipStream_t s) {
-    return out == Elem::f32 ? launch<Form::nt, Elem::f32>(a, s)
-                            : out == Elem::bf16 ? launch<Form::nt, Elem::bf16>(a, s) : launch<Form::nt, Elem::f16>(a, s);
-}
-hipError_t launch_i8_gated(const LayerArgs& a, Elem out, hipStream_t s) {
-    return out == Elem::bf16 ? launch<Form::gated, Elem::bf16>(a, s) : launch<Form::gated, Elem::f16>(a, s);
+    if (few_rows(a, 1, false)) return launch_i8_rows(a, false, out, s);
+    return out == Elem::f32 ? layer::launch_form<Form::nt, Elem::i8, Elem::f32>(a, s)
+                            : out == Elem::bf16 ? layer::launch_form<Form::nt, Elem::i8, Elem::bf16>(a, s)
+                                                : layer::launch_form<Form::nt, Elem::i8, Elem::f16>(a, s);
 }
 
 }  // namespace sgemm

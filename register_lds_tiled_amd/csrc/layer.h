@@ -67,6 +67,9 @@ hipError_t launch_i8_nt(const LayerArgs& a, Elem out, hipStream_t s);
 hipError_t launch_i8_gated(const LayerArgs& a, Elem out, hipStream_t s);
 // 16-bit operands and results.
 hipError_t launch_gated(const LayerArgs& a, Elem t, hipStream_t s);
+// The same for few rows of A, see few_rows in layer_rows.h.
+hipError_t launch_i8_rows(const LayerArgs& a, bool gated, Elem out, hipStream_t s);
+hipError_t launch_gated_rows(const LayerArgs& a, Elem t, hipStream_t s);
 hipError_t launch_gated_slopes(const GateArgs& a, Elem t, hipStream_t s);
 hipError_t launch_gated_dx(const LayerArgs& a, Elem t, hipStream_t s);
 hipError_t launch_gated_dw(const LayerArgs& a, Elem t, hipStream_t s);

@@ -1,0 +1,243 @@
+// layer_split.h -- small tiles of the feed-forward layer's products whose waves
+// divide k, and the choice of a product's tiles.
+//
+// For products with too few 128 x 128 tiles to fill the CUs (a batch in decoding,
+// a short prompt, narrow layers): a workgroup owns 32 to 64 rows and 64 or 128
+// columns of products, and each of its four waves the whole tile for every fourth
+// stage of 64 bytes of k.  A wave
+// brings its stages by DMA into a ring of its own in LDS, so the loop needs no
+// barrier, and nearly all of LDS is on its way from memory all the time: such
+// launches are bound by what the caches deliver and by its latency.  The waves'
+// parts are added at the end, in wave order, through LDS.
+#pragma once
+
+#include "layer_big.h"
+
+namespace sgemm {
+#ifdef __HIPCC__
+namespace layer {
+
+constexpr int kSplit = 4;   // waves
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "vmcnt");
+    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
+
+// T: the tile with one wave to all of it (WM = BM, WN = BN).
+template <class T, int RING>
+__global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int tiles_m, int tiles_n) {
+    constexpr int BM = T::BM, BN = T::BN, FM = T::FM, FN = T::FN, KST = T::KST, ES = T::ES;
+    constexpr int STAGE = T::SA + T::SB, MINE = RING * STAGE;
+    constexpr int AQ = T::SA / 1024, BQ = T::SB / 1024, NDMA = AQ + BQ;
+    constexpr int PART = BM * T::STR * 4;
+    static_assert(T::NW == 1 && PART <= MINE, "a wave's part of the result in its ring");
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[kSplit * MINE];
+    const int per = tiles_m * tiles_n;
+    const int out = T::OUTS == 2 && (int)blockIdx.x >= per ? 1 : 0;
+    int tm, tn;
+    tile_coords(blockIdx.x - out * per, tiles_m, tiles_n, T::GROUP_M, p.xcds, tm, tn);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int li = lane & 31, g = lane >> 5;
+    const long long m0 = (long long)tm * BM, n0 = (long long)tn * T::COLS;
+    const int mlast = (int)min((long long)p.M - 1 - m0, (long long)BM - 1);
+    const int nlast = (int)min((long long)p.N - 1 - n0, (long long)T::COLS - 1);
+    const unsigned ring = __builtin_amdgcn_readfirstlane(lds_addr(lds)) + (unsigned)(wave * MINE);
+
+    // Stages as in the large tiles' kernel: the first begins `pad` k below zero.
+    const int each = (int)(((long long)p.K + KST - 1) / KST), nst = each * T::PAIRS;
+    const int pad = (int)((long long)each * KST - p.K);
+    const int mine = (nst - wave + kSplit - 1) / kSplit;   // this wave's
+    auto along = [&](int v, int row, long long ld, int& kk) __attribute__((always_inline)) {
+        const int c = (lane & 3) ^ chunk_at(16 * v + (lane >> 2));
+        kk = 16 / ES * c;
+        return (unsigned)row * (unsigned)ld + 16u * (unsigned)c;
+    };
+    auto across = [&](int v, auto W, int last, long long ld, int& kk) __attribute__((always_inline)) {
+        const int k = v * (512 / W) + lane / (W / 8), c = lane % (W / 8) ^ across_swap<W>(k);
+        kk = k;
+        return (unsigned)k * (unsigned)ld + (8 * c <= last ? 16u * (unsigned)c : 0u);
+    };
+    const int pa = T::OUTS == 2 ? out : 0;
+    const unsigned char* const abase = T::A_ACROSS ? p.A[pa] + 2 * m0 : p.A[pa] + m0 * p.lda[pa];
+    const unsigned char* bbase[BQ];
+    unsigned aoff[AQ], boff[BQ];
+    int akk[AQ], bkk[BQ];
+#pragma unroll
+    for (int u = 0; u < AQ; ++u) {
+        if constexpr (T::A_ACROSS)
+            aoff[u] = across(u, std::integral_constant<int, BM>{}, mlast, p.lda[pa], akk[u]);
+        else
+            aoff[u] = along(u, min(16 * u + (lane >> 2), mlast), p.lda[pa], akk[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < BQ; ++u) {
+        if constexpr (T::B_ACROSS) {
+            bbase[u] = p.B[0] + 2 * n0;
+            boff[u] = across(u, std::integral_constant<int, BN>{}, nlast, p.ldb[0], bkk[u]);
+        } else {
+            int m = 0, row = 16 * u;
+            if constexpr (T::GATED) gated_row<T>(row, m, row);
+            bbase[u] = p.B[m] + n0 * p.ldb[m];
+            boff[u] = along(u, min(row + (lane >> 2), nlast), p.ldb[m], bkk[u]);
+        }
+    }
+    // Stage i of this wave into its place of the ring.
+    auto request = [&](int i) __attribute__((always_inline)) {
+        const int s = i * kSplit + wave;
+        const int pair = T::PAIRS == 2 && s >= each ? 1 : 0;
+        const long long k = (long long)(s - pair * each) * KST - pad;
+        const unsigned char* const a = abase + (T::A_ACROSS ? k * p.lda[pa] : k * ES) + (pair ? p.A[1] - p.A[0] : 0);
+        const long long b = (T::B_ACROSS ? k * p.ldb[0] : k * ES) + (pair ? p.B[1] - p.B[0] : 0);
+        const unsigned to = ring + (unsigned)(i % RING * STAGE);
+        if (s == 0 && pad > 0) {   // lanes below k = 0 copy zeros
+            const unsigned char* const zero = reinterpret_cast<const unsigned char*>(&kZero16);
+#pragma unroll
+            for (int u = 0; u < AQ; ++u)
+                lds_dma16(akk[u] >= pad ? a + aoff[u] : zero, __builtin_amdgcn_readfirstlane(to + 1024u * u));
+#pragma unroll
+            for (int u = 0; u < BQ; ++u)
+                lds_dma16(bkk[u] >= pad ? bbase[u] + b + boff[u] : zero,
+                          __builtin_amdgcn_readfirstlane(to + T::SA + 1024u * u));
+        } else {
+#pragma unroll
+            for (int u = 0; u < AQ; ++u) lds_dma16s(a, aoff[u], __builtin_amdgcn_readfirstlane(to + 1024u * u));
+#pragma unroll
+            for (int u = 0; u < BQ; ++u)
+                lds_dma16s(bbase[u] + b, boff[u], __builtin_amdgcn_readfirstlane(to + T::SA + 1024u * u));
+        }
+    };
+    uint4 a[2][FM], b[2][FN];
+    auto read = [&](int i) __attribute__((always_inline)) {
+        const unsigned char* const st = lds + wave * MINE + i % RING * STAGE;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                if constexpr (T::A_ACROSS)
+                    a[t][j] = read_across<BM>(st + across_at<BM>(0, j, t, lane));
+                else
+                    a[t][j] = *reinterpret_cast<const uint4*>(st + along_at(0, j, t, li, g));
+            }
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                if constexpr (T::B_ACROSS)
+                    b[t][j] = read_across<BN>(st + T::SA + across_at<BN>(0, j, t, lane));
+                else
+                    b[t][j] = *reinterpret_cast<const uint4*>(st + T::SA + along_at(0, j, t, li, g));
+            }
+        }
+        // the stage is in registers: its place is free
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    acc_of<T::E> acc[FM][FN] = {};
+    auto multiply = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = mfma<T::E>(a[t][i], b[t][j], acc[i][j]);
+    };
+#pragma unroll
+    for (int i = 0; i < RING; ++i)
+        if (i < mine) request(i);
+    int i = 0;
+    for (; i + RING < mine; ++i) {
+        wait_loads<(RING - 1) * NDMA>();
+        read(i);
+        request(i + RING);
+        multiply();
+    }
+    wait_loads<0>();
+    for (; i < mine; ++i) {
+        read(i);
+        multiply();
+    }
+    float* const part = reinterpret_cast<float*>(lds + wave * MINE);
+    lane_order();
+    static_for<FM>([&](auto m) __attribute__((always_inline)) { put_rows<T>(acc[m], part + m * 32 * T::STR, li, g); });
+    __syncthreads();
+    // a thread has the same eight columns in every row of its
+    constexpr int UNITS = T::COLS / 8, STEP = 64 * kSplit / UNITS;
+    const int u = threadIdx.x % UNITS;
+    const long long at = n0 + 8 * u;
+    const int n = (int)min(p.N - at, 8ll);
+    if (n <= 0) return;
+    Scales8 s;
+    load_scales<T>(p, at, n, s);
+    for_act<T>(p, [&](auto act) __attribute__((always_inline)) {
+        for (int row = threadIdx.x / UNITS; row < min(BM, mlast + 1); row += STEP) {
+            const long long R = m0 + row;
+            const float sa = T::E == Elem::i8 && p.K > 0 ? p.SA[R] : 0.f;
+            float x[8], y[8];
+            auto sum = [&](float (&v)[8], int c) __attribute__((always_inline)) {
+                const unsigned char* const from = lds + 4 * (row * T::STR + c);
+                __builtin_memcpy(v, from, 32);
+#pragma unroll
+                for (int w = 1; w < kSplit; ++w) {
+                    float z[8];
+                    __builtin_memcpy(z, from + w * MINE, 32);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if constexpr (T::E == Elem::i8)
+                            v[e] = __int_as_float(__float_as_int(v[e]) + __float_as_int(z[e]));
+                        else
+                            v[e] += z[e];
+                    }
+                }
+            };
+            sum(x, 8 * u);
+            if constexpr (T::GATED) sum(y, T::COLS + 8 * u);
+            finish8<T, act>(p, out, R, at, n, sa, s, x, y);
+        }
+    });
+}
+
+template <class T, int RING>
+hipError_t launch_split(const LayerArgs& a, hipStream_t s) {
+    const long long tm = ((long long)a.M + T::BM - 1) / T::BM, tn = ((long long)a.N + T::COLS - 1) / T::COLS;
+    if (tm * tn * T::OUTS * 64 * kSplit > 0xFFFFFFFFll) return hipErrorInvalidValue;
+    split_kernel<T, RING><<<(unsigned)(tm * tn * T::OUTS), 64 * kSplit, 0, s>>>(a, (int)tm, (int)tn);
+    return hipGetLastError();
+}
+
+// A product's tiles.  Of those whose waves divide k the smallest that fits one
+// round of workgroups, one to a CU; else 128 x 128 up to two to a CU, and 256 x
+// 256 beyond.  us, K = 4096 (the next larger choice in brackets): int8 64 x 4096
+// 8.9 (12.6), 128 x 4096 11.9 (17.4), 512 x 4096 19.5 (21.1), 1024 x 4096 23.5
+// (48.9); gated bf16 64 x 4096 25 (34), 128 x 4096 31 (43), 512 x 2048 34 (47), 1024
+// x 4096 73 (92), 1024 x 8192 147 and 111; dX 512 x 4096 59 (99).
+// Rows off 16 bytes go through registers, in 64 x 64 (gated: x 128) products where
+// 128 x 128 would not give every CU two (1000 x 1500 x 777 int8 11.0 against 18.6,
+// dX 40 against 69; 2047^3 int8 33 against 31, dX 146 against 194).
+template <Form F, Elem E, Elem OUT>
+hipError_t launch_form(const LayerArgs& a, hipStream_t s) {
+    using Wide = Tile<F, E, OUT, 256, 256, 128, 128, 4>;
+    using Mid = Tile<F, E, OUT, 128, 128, 64, 64>;
+    constexpr bool G = F == Form::gated;
+    auto tiles = [&](auto t) {
+        using T = decltype(t);
+        return ((long long)a.M + T::BM - 1) / T::BM * (((long long)a.N + T::COLS - 1) / T::COLS) * T::OUTS;
+    };
+    if (!big_fits<Mid>(a)) {
+        using Small = Tile<F, E, OUT, 64, G ? 128 : 64, 32, G ? 64 : 32>;
+        if (tiles(Mid{}) <= a.cus) return launch_tiles<Small>(tile_kernel<Small>, a, s);
+        return launch_tiles<Mid>(tile_kernel<Mid>, a, s);
+    }
+    using S32 = Tile<F, E, OUT, 32, 64, 32, 64>;
+    using S64 = Tile<F, E, OUT, 64, 64, 64, 64>;
+    using S128 = Tile<F, E, OUT, 64, 128, 64, 128>;
+    if (tiles(S32{}) <= a.cus) return launch_split<S32, 3>(a, s);
+    if (tiles(S64{}) <= a.cus) return launch_split<S64, 3>(a, s);
+    if (tiles(S128{}) <= a.cus) return launch_split<S128, 3>(a, s);
+    if (tiles(Mid{}) <= 2ll * a.cus) return launch_tiles<Mid>(big_kernel<Mid>, a, s);
+    return launch_tiles<Wide>(big_kernel<Wide>, a, s);
+}
+
+}  // namespace layer
+#endif
+}  // namespace sgemm

@@ -14,8 +14,9 @@
 // their chunk_at differ.
 //
 // An operand of 16-bit elements whose rows run across k lies as 32 k rows of W
-// columns, chunk c of row k at c ^ 4 (k % 4), and comes out of LDS through the
-// transposing read: within 16 lanes, element e of lane i is element i % 4 of the
+// columns, chunk c of row k at c ^ across_swap(k): the four rows that one read
+// takes 64 bytes of then lie in the window's four places.  It comes out of LDS
+// through the transposing read: within 16 lanes, element e of lane i is element i % 4 of the
 // 8 bytes that lane 4e + i / 4 addresses.
 //
 // The gated form multiplies two matrices by the same rows of A: of a wave's
@@ -30,6 +31,9 @@ namespace sgemm {
 namespace layer {
 
 __device__ __forceinline__ int chunk_at(int r) { return r >> 3 & 3; }
+// Four rows of 32 columns fill the window, two of 64, one of 128 and more.
+template <int W>
+__device__ __forceinline__ int across_swap(int k) { return W == 32 ? 0 : W == 64 ? k << 1 & 4 : (k & 3) << 2; }
 
 template <Elem E>
 using acc_of = std::conditional_t<E == Elem::i8, intx16, floatx16>;
@@ -57,72 +61,126 @@ struct Tile {
     static constexpr bool GATED = F == Form::gated;
     static constexpr bool A_ACROSS = F == Form::both, B_ACROSS = F == Form::sum2 || F == Form::both;
     static constexpr int ES = size_of<E>, KST = 64 / ES;          // k of a stage
-    static constexpr int SA = BM * 64, SB = BN * 64;              // bytes of a stage
+    static constexpr int SA = BM * 64, SB = BN * 64;              // bytes of 64 of k
     static constexpr int COLS = GATED ? BN / 2 : BN;              // columns of C
     static constexpr int PAIRS = F == Form::sum2 ? 2 : 1;
     static constexpr int OUTS = F == Form::both ? 2 : 1;
     // the epilogue's rows: 32 of WN values, rows four apart in the other half of the banks
     static constexpr int STR = WN + 8;
-    static constexpr int EPI = NW * 32 * STR * 4;                 // bytes
+    static constexpr int EPI = NW * (32 * STR + WM + WN) * 4;     // bytes, with the scales
     static_assert(4 * STR % 64 == 32, "rows four apart");
     static_assert(!GATED || WN % 64 == 0, "two halves of whole blocks");
 };
 
-// A wave's outputs from its accumulators: 32 rows at a time through LDS (mine:
-// 32 STR words of the wave's own), so that a lane has eight neighbouring columns
-// and stores them whole.  r0, c0: the first row and column of C.
-template <class T, class Acc>
-__device__ __forceinline__ void epilogue(const LayerArgs& p, int out, const Acc (&acc)[T::FM][T::FN], float* mine,
-                                         long long r0, long long c0, int lane) {
-    constexpr int WCOLS = T::GATED ? T::WN / 2 : T::WN;   // columns of C in a wave
-    constexpr int UNITS = WCOLS / 8;
-    const int li = lane & 31, g = lane >> 5;
-    const long long cols = p.N - c0;
+// The scales of eight columns from `at` on, n (1 and up) of them in the matrix.
+struct Scales8 {
+    float x[8], y[8];
+};
+template <class T>
+__device__ __forceinline__ void load_scales(const LayerArgs& p, long long at, int n, Scales8& s) {
+    if constexpr (T::E == Elem::i8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const long long c = at + min(e, n - 1);
+            s.x[e] = p.K > 0 ? p.SB[0][c] : 0.f;
+            if constexpr (T::GATED) s.y[e] = p.K > 0 ? p.SB[1][c] : 0.f;
+        }
+    }
+}
+// Eight neighbouring outputs of row R from column `at` on, n (1 and up) of them
+// in the matrix: the sums x (whole numbers in the registers of floats where the
+// operands are), in the gated form the second matrix's in y.
+template <class T, int ACT>
+__device__ __forceinline__ void finish8(const LayerArgs& p, int out, long long R, long long at, int n, float sa,
+                                        const Scales8& s, float (&x)[8], float (&y)[8]) {
     typedef type_of<T::OUT> O;
-    O* const C = static_cast<O*>(p.C[out]);
+    if constexpr (T::E == Elem::i8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = (float)__float_as_int(x[e]) * sa * s.x[e];
+            if constexpr (T::GATED) y[e] = (float)__float_as_int(y[e]) * sa * s.y[e];
+        }
+    }
+    if constexpr (T::GATED) {
+        if constexpr (T::E != Elem::i8)
+            if (p.G != nullptr) {
+                store8<T::OUT>(static_cast<O*>(p.G) + R * p.ldg + at, x, n);
+                store8<T::OUT>(static_cast<O*>(p.U) + R * p.ldu + at, y, n);
+            }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = act_of<ACT>(x[e]) * y[e];
+    }
+    store8<T::OUT>(static_cast<O*>(p.C[out]) + R * p.ldc[out] + at, x, n);
+}
+// f(integral_constant of the activation), none where there is no gate.
+template <class T, class F>
+__device__ __forceinline__ void for_act(const LayerArgs& p, F&& f) {
+    if constexpr (T::GATED)
+        with_act(p.act, f);
+    else
+        f(std::integral_constant<int, 0>{});
+}
+
+// A 32-row piece of accumulators to LDS, rows STR words apart.
+template <class T, class Acc>
+__device__ __forceinline__ void put_rows(const Acc (&acc)[T::FN], float* to, int li, int g) {
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const auto v = acc[j][r];   // (a bit cast of the element itself would take the vector's first)
+            to[(8 * (r / 4) + 4 * g + r % 4) * T::STR + 32 * j + li] = __builtin_bit_cast(float, v);
+        }
+}
+
+// A wave's outputs from its accumulators: 32 rows at a time through LDS (mine:
+// 32 STR + WM + WN words of the wave's own), so that a lane has eight neighbouring
+// columns and stores them whole.  r0, c0: the first row and column of C.  The
+// scales come to LDS before the first row: loaded row by row they cost 8192^3
+// int8 40 us.
+template <class T, class Acc>
+__device__ __forceinline__ void epilogue(const LayerArgs& p, int out, const Acc (&acc)[T::FM][T::FN], float* lds,
+                                         int wave, long long r0, long long c0, int lane) {
+    constexpr int WCOLS = T::GATED ? T::WN / 2 : T::WN;   // columns of C in a wave
+    constexpr int UNITS = WCOLS / 8, STEP = 64 / UNITS;
+    float *const mine = lds + wave * (32 * T::STR + T::WM + T::WN), *const row_scales = mine + 32 * T::STR,
+                *const col_scales = row_scales + T::WM;
+    const int u = lane % UNITS, row0 = lane / UNITS;
+    const long long at = c0 + 8 * u;
+    const int n = (int)min(p.N - at, 8ll);
+    if constexpr (T::E == Elem::i8) {
+        if (p.K > 0) {
+            for (int r = lane; r < T::WM; r += 64) row_scales[r] = p.SA[min(r0 + r, (long long)p.M - 1)];
+            for (int c = lane; c < T::WN; c += 64) {
+                const int m = T::GATED ? c / WCOLS : 0;
+                col_scales[c] = p.SB[m][min(c0 + c - m * WCOLS, (long long)p.N - 1)];
+            }
+        } else {
+            for (int r = lane; r < T::WM + T::WN; r += 64) row_scales[r] = 0.f;
+        }
+    }
     static_for<T::FM>([&](auto i) __attribute__((always_inline)) {
         lane_order();
-#pragma unroll
-        for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const auto v = acc[i][j][r];   // (a bit cast of the element itself would take the vector's first)
-                mine[(8 * (r / 4) + 4 * g + r % 4) * T::STR + 32 * j + li] = __builtin_bit_cast(float, v);
-            }
+        put_rows<T>(acc[i], mine, lane & 31, lane >> 5);
         lane_order();
+        for_act<T>(p, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll 1
-        for (int id = lane; id < 32 * UNITS; id += 64) {
-            const int row = id / UNITS, u = id % UNITS;
-            const long long R = r0 + 32 * i + row;
-            const int n = (int)min(cols - 8 * u, 8ll);
-            if (R >= p.M || n <= 0) continue;
-            float x[8], y[8];
-            const float* const from = mine + row * T::STR + 8 * u;
-            __builtin_memcpy(x, from, 32);
-            if constexpr (T::GATED) __builtin_memcpy(y, from + WCOLS, 32);
-            if constexpr (T::E == Elem::i8) {
-                const float sa = p.K > 0 ? p.SA[R] : 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const long long c = c0 + 8 * u + min(e, n - 1);
-                    x[e] = (float)__float_as_int(x[e]) * sa * (p.K > 0 ? p.SB[0][c] : 0.f);
-                    if constexpr (T::GATED) y[e] = (float)__float_as_int(y[e]) * sa * (p.K > 0 ? p.SB[1][c] : 0.f);
+            for (int row = row0; row < 32; row += STEP) {
+                const long long R = r0 + 32 * i + row;
+                if (R >= p.M || n <= 0) continue;
+                float x[8], y[8], sa = 0.f;
+                Scales8 s;
+                const float* const from = mine + row * T::STR + 8 * u;
+                __builtin_memcpy(x, from, 32);
+                if constexpr (T::GATED) __builtin_memcpy(y, from + WCOLS, 32);
+                if constexpr (T::E == Elem::i8) {
+                    sa = row_scales[32 * i + row];
+                    __builtin_memcpy(s.x, col_scales + 8 * u, 32);
+                    if constexpr (T::GATED) __builtin_memcpy(s.y, col_scales + WCOLS + 8 * u, 32);
                 }
+                finish8<T, act>(p, out, R, at, n, sa, s, x, y);
             }
-            const long long at = c0 + 8 * u;
-            if constexpr (T::GATED) {
-                if constexpr (T::E != Elem::i8)
-                    if (p.G != nullptr) {
-                        store8<T::OUT>(static_cast<O*>(p.G) + R * p.ldg + at, x, n);
-                        store8<T::OUT>(static_cast<O*>(p.U) + R * p.ldu + at, y, n);
-                    }
-                with_act(p.act, [&](auto a) __attribute__((always_inline)) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = act_of<a>(x[e]) * y[e];
-                });
-            }
-            store8<T::OUT>(C + R * p.ldc[out] + at, x, n);
-        }
+        });
     });
 }
 
@@ -132,11 +190,12 @@ __device__ __forceinline__ int along_at(int w, int j, int t, int li, int g) {
     return (w + 32 * j + li) * 64 + 16 * ((2 * g + t) ^ chunk_at(li));
 }
 // The lower read of two (k .. k + 3 of the lane's eight); the upper is 4 rows on.
-template <int W>
+// HALF: the k rows of one lane half.
+template <int W, int HALF = 16>
 __device__ __forceinline__ int across_at(int w, int j, int t, int lane) {
     const int q = lane >> 4, e = (lane >> 2) & 3, n = lane & 3;
-    const int k = 16 * (q >> 1) + e + 8 * t, col = w + 32 * j + 16 * (q & 1) + 4 * n;
-    return 2 * (k * W + (((col >> 3) ^ (4 * e)) << 3 | (col & 7)));
+    const int k = HALF * (q >> 1) + e + 8 * t, col = w + 32 * j + 16 * (q & 1) + 4 * n;
+    return 2 * (k * W + (((col >> 3) ^ across_swap<W>(e)) << 3 | (col & 7)));
 }
 template <int W>
 __device__ __forceinline__ uint4 read_across(const unsigned char* at) {
@@ -157,15 +216,15 @@ __device__ __forceinline__ void gated_row(int r, int& m, int& row) {
     row = r / T::WN * H + r % H;
 }
 
-// Tiles through registers: any alignment, pitch and length.  Two LDS stages, one
-// barrier a stage: the next stage is loaded while one multiplies, and written to
-// the other place behind it.
+// Tiles through registers: any alignment, pitch and length.  128 bytes of k at a
+// time, in two LDS places: the next ones are loaded while one multiplies, and
+// written to the other place behind it, so there is one barrier to 128 bytes.
 template <class T>
 __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m, int tiles_n) {
-    constexpr int BM = T::BM, BN = T::BN, NT = T::NT, FM = T::FM, FN = T::FN, KST = T::KST;
-    constexpr int CA = BM * 4 / NT, CB = BN * 4 / NT;             // a thread's chunks
-    static_assert(CA * NT == BM * 4 && CB * NT == BN * 4, "whole rounds of the loader");
-    constexpr int STAGE = T::SA + T::SB, ROOM = 2 * STAGE > T::EPI ? 2 * STAGE : T::EPI;
+    constexpr int BM = T::BM, BN = T::BN, NT = T::NT, FM = T::FM, FN = T::FN, KST = 2 * T::KST;
+    constexpr int CA = BM * 8 / NT, CB = BN * 8 / NT;             // a thread's chunks
+    static_assert(CA * NT == BM * 8 && CB * NT == BN * 8, "whole rounds of the loader");
+    constexpr int STAGE = 2 * (T::SA + T::SB), ROOM = 2 * STAGE > T::EPI ? 2 * STAGE : T::EPI;
     __shared__ __attribute__((aligned(16))) unsigned char lds[ROOM];
     const int per = tiles_m * tiles_n;
     const int out = T::OUTS == 2 && (int)blockIdx.x >= per ? 1 : 0;
@@ -177,40 +236,75 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
     const int li = lane & 31, g = lane >> 5;
     const long long m0 = (long long)tm * BM, n0 = (long long)tn * T::COLS;
     const long long row_bytes = (long long)p.K * T::ES;
-    const long long each = ((long long)p.K + KST - 1) / KST, stages = each * T::PAIRS;
+    const int each = (int)(((long long)p.K + KST - 1) / KST), stages = each * T::PAIRS;
+    // Stages of whole k, in tiles whose columns across are whole: plain loads.
+    const int whole = (!T::A_ACROSS || m0 + BM <= p.M) && (!T::B_ACROSS || n0 + BN <= p.N) ? p.K / KST : 0;
 
-    // A chunk of an operand whose rows run along k (row of its matrix), or
-    // across it (k row, and the byte of its first column).
-    auto along = [&](const unsigned char* M, long long ld, long long row, long long s, int c) {
-        return mx_bytes16(M + row * ld, s * 64 + 16 * c, row_bytes);
-    };
-    auto across = [&](const unsigned char* M, long long ld, long long k, long long at, long long len) {
-        return k < p.K ? mx_bytes16(M + k * ld, at, len) : make_uint4(0u, 0u, 0u, 0u);
-    };
+    // The thread's chunk u of an operand: its row (or k row) and place in it.  Rows
+    // past a matrix read its last one: their products are not stored.
+    auto along_row = [&](int id) { return id >> 3; };
+    long long arow[CA], brow[CB];           // bytes from the first matrix's start to the row's
+#pragma unroll
+    for (int u = 0; u < CA; ++u) {
+        const int id = tid + u * NT;
+        arow[u] = T::A_ACROSS ? 2 * m0 : min(m0 + along_row(id), (long long)p.M - 1) * p.lda[0];
+    }
+#pragma unroll
+    for (int u = 0; u < CB; ++u) {
+        const int id = tid + u * NT;
+        int m = 0, row = along_row(id);
+        if constexpr (T::GATED) gated_row<T>(row, m, row);
+        brow[u] = T::B_ACROSS ? 2 * n0
+                              : (m ? p.B[1] - p.B[0] : 0) + min(n0 + row, (long long)p.N - 1) * (m ? p.ldb[1] : p.ldb[0]);
+    }
     uint4 va[CA], vb[CB];
-    auto fetch = [&](long long s) __attribute__((always_inline)) {
+    auto fetch = [&](int s) __attribute__((always_inline)) {
         const int pair = T::PAIRS == 2 && s >= each ? 1 : 0;
-        const long long st = s - pair * each;
+        const int st = s - pair * each;
         const int ma = T::OUTS == 2 ? out : pair;
+        const unsigned char *const A = p.A[ma], *const B = p.B[pair];
+        const long long lda = p.lda[ma], ldb = p.ldb[pair], k0 = (long long)st * KST;
+        auto a_row = [&](int u) __attribute__((always_inline)) {
+            if constexpr (T::A_ACROSS || T::PAIRS == 1) return arow[u];
+            return min(m0 + along_row(tid + u * NT), (long long)p.M - 1) * lda;
+        };
+        auto load = [&](auto plain) __attribute__((always_inline)) {
+            auto get = [&](const unsigned char* row, long long at, long long len) __attribute__((always_inline)) {
+                if constexpr (plain) {
+                    uint4 v;
+                    __builtin_memcpy(&v, row + at, 16);
+                    return v;
+                } else {
+                    return mx_bytes16(row, at, len);
+                }
+            };
 #pragma unroll
-        for (int u = 0; u < CA; ++u) {
-            const int id = tid + u * NT;
-            if constexpr (T::A_ACROSS)
-                va[u] = across(p.A[ma], p.lda[ma], st * KST + id / (BM / 8), 2 * m0 + 16 * (id % (BM / 8)), 2ll * p.M);
-            else
-                va[u] = along(p.A[ma], p.lda[ma], min(m0 + (id >> 2), (long long)p.M - 1), st, id & 3);
-        }
-#pragma unroll
-        for (int u = 0; u < CB; ++u) {
-            const int id = tid + u * NT;
-            if constexpr (T::B_ACROSS) {
-                vb[u] = across(p.B[pair], p.ldb[pair], st * KST + id / (BN / 8), 2 * n0 + 16 * (id % (BN / 8)), 2ll * p.N);
-            } else {
-                int m = 0, row = id >> 2;
-                if constexpr (T::GATED) gated_row<T>(id >> 2, m, row);
-                vb[u] = along(m ? p.B[1] : p.B[0], m ? p.ldb[1] : p.ldb[0], min(n0 + row, (long long)p.N - 1), st, id & 3);
+            for (int u = 0; u < CA; ++u) {
+                const int id = tid + u * NT;
+                if constexpr (T::A_ACROSS) {
+                    const long long k = k0 + id / (BM / 8);
+                    va[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (plain || k < p.K) va[u] = get(A + k * lda, 2 * m0 + 16 * (id % (BM / 8)), 2ll * p.M);
+                } else {
+                    va[u] = get(A + a_row(u), k0 * T::ES + 16 * (id & 7), row_bytes);
+                }
             }
-        }
+#pragma unroll
+            for (int u = 0; u < CB; ++u) {
+                const int id = tid + u * NT;
+                if constexpr (T::B_ACROSS) {
+                    const long long k = k0 + id / (BN / 8);
+                    vb[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (plain || k < p.K) vb[u] = get(B + k * ldb, 2 * n0 + 16 * (id % (BN / 8)), 2ll * p.N);
+                } else {
+                    vb[u] = get(B + brow[u], k0 * T::ES + 16 * (id & 7), row_bytes);
+                }
+            }
+        };
+        if (st < whole)
+            load(std::true_type{});
+        else
+            load(std::false_type{});
     };
     auto place = [&](int buf) __attribute__((always_inline)) {
         unsigned char* const to = lds + buf * STAGE;
@@ -218,21 +312,20 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
             lds_poison_f4(at);
             *reinterpret_cast<uint4*>(at) = v;
         };
+        // 64 bytes of k behind the others
+        auto along = [](int id, int S) { return (id >> 2 & 1) * S + (id >> 3) * 64 + 16 * ((id & 3) ^ chunk_at(id >> 3)); };
+        auto across = [](int id, auto W) {
+            return id / (W / 8) * (2 * W) + 16 * (id % (W / 8) ^ across_swap<W>(id / (W / 8)));
+        };
 #pragma unroll
         for (int u = 0; u < CA; ++u) {
             const int id = tid + u * NT;
-            if constexpr (T::A_ACROSS)
-                put(to + id / (BM / 8) * (2 * BM) + 16 * (id % (BM / 8) ^ 4 * (id / (BM / 8) & 3)), va[u]);
-            else
-                put(to + (id >> 2) * 64 + 16 * ((id & 3) ^ chunk_at(id >> 2)), va[u]);
+            put(to + (T::A_ACROSS ? across(id, std::integral_constant<int, BM>{}) : along(id, T::SA)), va[u]);
         }
 #pragma unroll
         for (int u = 0; u < CB; ++u) {
             const int id = tid + u * NT;
-            if constexpr (T::B_ACROSS)
-                put(to + T::SA + id / (BN / 8) * (2 * BN) + 16 * (id % (BN / 8) ^ 4 * (id / (BN / 8) & 3)), vb[u]);
-            else
-                put(to + T::SA + (id >> 2) * 64 + 16 * ((id & 3) ^ chunk_at(id >> 2)), vb[u]);
+            put(to + 2 * T::SA + (T::B_ACROSS ? across(id, std::integral_constant<int, BN>{}) : along(id, T::SB)), vb[u]);
         }
     };
 
@@ -242,35 +335,36 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
         place(0);
     }
     __syncthreads();
-    for (long long s = 0; s < stages; ++s) {
+    for (int s = 0; s < stages; ++s) {
         if (s + 1 < stages) fetch(s + 1);
         const unsigned char* const st = lds + (s & 1) * STAGE;
-        static_for<2>([&](auto t) __attribute__((always_inline)) {
+        static_for<4>([&](auto h) __attribute__((always_inline)) {
+            constexpr int t = h % 2;
+            const unsigned char *const sa = st + h / 2 * T::SA, *const sb = st + 2 * T::SA + h / 2 * T::SB;
             uint4 a[FM], b[FN];
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 if constexpr (T::A_ACROSS)
-                    a[i] = read_across<BM>(st + across_at<BM>(wm, i, t, lane));
+                    a[i] = read_across<BM>(sa + across_at<BM>(wm, i, t, lane));
                 else
-                    a[i] = *reinterpret_cast<const uint4*>(st + along_at(wm, i, t, li, g));
+                    a[i] = *reinterpret_cast<const uint4*>(sa + along_at(wm, i, t, li, g));
             }
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 if constexpr (T::B_ACROSS)
-                    b[j] = read_across<BN>(st + T::SA + across_at<BN>(wn, j, t, lane));
+                    b[j] = read_across<BN>(sb + across_at<BN>(wn, j, t, lane));
                 else
-                    b[j] = *reinterpret_cast<const uint4*>(st + T::SA + along_at(wn, j, t, li, g));
+                    b[j] = *reinterpret_cast<const uint4*>(sb + along_at(wn, j, t, li, g));
             }
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int j = 0; j < FN; ++j) acc[i][j] = mfma<T::E>(a[i], b[j], acc[i][j]);
         });
-        if (s + 1 < stages) place((int)((s + 1) & 1));
+        if (s + 1 < stages) place((s + 1) & 1);
         __syncthreads();
     }
-    epilogue<T>(p, out, acc, reinterpret_cast<float*>(lds) + wave * 32 * T::STR, m0 + wm,
-                n0 + (T::GATED ? wn / 2 : wn), lane);
+    epilogue<T>(p, out, acc, reinterpret_cast<float*>(lds), wave, m0 + wm, n0 + (T::GATED ? wn / 2 : wn), lane);
 }
 
 // One workgroup per tile; more threads than a launch holds are refused by the
