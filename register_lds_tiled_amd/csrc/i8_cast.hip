@@ -3,17 +3,21 @@
 //
 // s = max(fl(t / 127), 2^-126) for a row whose largest magnitude is t, and
 // q = x / s rounded to nearest, ties to even: |q| <= 127, since t / s is at most
-// 127 (1 + 2^-24).  The quotient's rounding is exact without a division: x
-// times the reciprocal of s is near enough that its rounding q' is off by one at
-// most, x - q' s has few enough bits for one fused multiply-add to be exact (x
-// and q' s are multiples of s's last bit where |x| >= s, their difference no
-// larger than s; below that q' is 0 or +-1, and the difference is x or that of
-// two numbers within a factor of two; just below s / 2 it may round to s / 2,
-// and the tie goes to 0 as it should), and twice it is compared with s.
+// 127 (1 + 2^-24).  The quotient is not divided out: x times the reciprocal of s,
+// added to 3 2^22, leaves in the sum's low byte a whole number q' that is off by
+// one at most, and only next to a half.  The rest x - q' s has few enough bits for
+// one fused multiply-add to be exact (x and q' s are multiples of s's last bit
+// where |x| >= s, their difference no larger than s; below that q' is 0 or +-1,
+// and the difference is x or that of two numbers within a factor of two; just
+// below s / 2 it may round to s / 2, and the tie goes to 0 as it should).  Where
+// no rest of eight values reaches s / 2 all are right; else they are put right
+// one by one.
 //
 // Bound by memory: X is read once (rows of up to kHeld units a thread stay in
-// registers between the maximum and the rounding), Q and S are written once.
-// Threads share a row, or a wave takes a row of its own where rows are short.
+// registers between the maximum and the rounding), Q and S are written once; but
+// seven vector instructions a value come near (with twenty 8192^2 bf16 took 78
+// us).  Threads share a row, or a wave takes a row of its own where rows are
+// short.
 #include "layer.h"
 
 namespace sgemm {
@@ -48,14 +52,40 @@ __device__ __forceinline__ void values(const Unit<T>& u, float (&x)[8]) {
         unpack8<T>(make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]), x);
     }
 }
-// The largest magnitude's bits: infinities and NaN are past every number's.
+// The largest magnitude's bits in the type's own pattern, where infinities and
+// NaN are past every number's: 16-bit types keep two of them, side by side.
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 template <Elem T>
 __device__ __forceinline__ unsigned top_of(const Unit<T>& u, unsigned top) {
-    float x[8];
-    values(u, x);
+    if constexpr (T == Elem::f32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    return top;
+        for (int i = 0; i < 8; ++i) top = max(top, u.w[i] & 0x7FFFFFFFu);
+        return top;
+    } else {
+        u16x2 t = __builtin_bit_cast(u16x2, top);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2, u.w[i] & 0x7FFF7FFFu));
+        return __builtin_bit_cast(unsigned, t);
+    }
+}
+// The larger of two such maxima; the value of one as a float, and whether it is
+// a number.
+template <Elem T>
+__device__ __forceinline__ unsigned larger(unsigned a, unsigned b) {
+    if constexpr (T == Elem::f32) return max(a, b);
+    return __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+template <Elem T>
+__device__ __forceinline__ float top_value(unsigned top, bool& finite) {
+    if constexpr (T == Elem::f32) {
+        finite = top < 0x7F800000u;
+        return __uint_as_float(top);
+    } else {
+        const unsigned t = max(top & 0xFFFFu, top >> 16);
+        finite = t < (T == Elem::bf16 ? 0x7F80u : 0x7C00u);
+        return T == Elem::bf16 ? __uint_as_float(t << 16) : (float)__builtin_bit_cast(_Float16, (unsigned short)t);
+    }
 }
 __device__ __forceinline__ int quotient(float x, float s, float inverse) {
     float q = __builtin_rintf(x * inverse);
@@ -67,13 +97,25 @@ __device__ __forceinline__ int quotient(float x, float s, float inverse) {
 template <Elem T>
 __device__ __forceinline__ void store_unit(const Unit<T>& u, signed char* row, int i, int C, float s, float inverse,
                                            bool finite) {
-    float x[8];
+    constexpr float MAGIC = 12582912.f;   // 3 2^22: the last bit of the sum is 1
+    float x[8], rest = 0.f;
+    unsigned y[8], b[2];
     values(u, x);
-    unsigned b[2] = {0u, 0u};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const int q = finite ? quotient(x[e], s, inverse) : 0;
-        b[e / 4] |= ((unsigned)q & 255u) << (8 * (e % 4));
+        const float f = __builtin_fmaf(x[e], inverse, MAGIC);
+        y[e] = __float_as_uint(f);
+        rest = fmaxf(rest, __builtin_fabsf(__builtin_fmaf(MAGIC - f, s, x[e])));
+    }
+    if (!(rest < 0.5f * s) || !finite) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = finite ? (unsigned)quotient(x[e], s, inverse) : 0u;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // the low bytes
+        const unsigned lo = __builtin_amdgcn_perm(y[4 * h + 1], y[4 * h], 0x0C0C0400u);
+        const unsigned hi = __builtin_amdgcn_perm(y[4 * h + 3], y[4 * h + 2], 0x04000C0Cu);
+        b[h] = lo | hi;
     }
     signed char* const to = row + 8ll * i;
     const int n = C - 8 * i;
@@ -113,17 +155,17 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void i8_quantize_kernel(I8Cast
             top = top_of<T>(u, top);
         }
 #pragma unroll
-        for (int d = 32; d > 0; d /= 2) top = max(top, (unsigned)__shfl_xor((int)top, d));
+        for (int d = 32; d > 0; d /= 2) top = larger<T>(top, (unsigned)__shfl_xor((int)top, d));
         if constexpr (NW > 1) {
             // two places in turn, so that a row's are read before they are written again
             if (threadIdx.x % 64 == 0) tops[turn & 1][threadIdx.x / 64] = top;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < NW; ++w) top = max(top, tops[turn & 1][w]);
+            for (int w = 0; w < NW; ++w) top = larger<T>(top, tops[turn & 1][w]);
             ++turn;
         }
-        const bool finite = top < 0x7F800000u;
-        const float s = fmaxf(__uint_as_float(top) / 127.f, 0x1p-126f), inverse = 1.f / s;
+        bool finite;
+        const float s = fmaxf(top_value<T>(top, finite) / 127.f, 0x1p-126f), inverse = 1.f / s;
         signed char* const to = static_cast<signed char*>(p.Q) + r * p.ldq;
 #pragma unroll
         for (int h = 0; h < kHeld<T>; ++h)

@@ -212,8 +212,9 @@ hipError_t launch_split(const LayerArgs& a, hipStream_t s) {
 // (48.9); gated bf16 64 x 4096 25 (34), 128 x 4096 31 (43), 512 x 2048 34 (47), 1024
 // x 4096 73 (92), 1024 x 8192 147 and 111; dX 512 x 4096 59 (99).
 // Rows off 16 bytes go through registers, in 64 x 64 (gated: x 128) products where
-// 128 x 128 would not give every CU two (1000 x 1500 x 777 int8 11.0 against 18.6,
-// dX 40 against 69; 2047^3 int8 33 against 31, dX 146 against 194).
+// 128 x 128 would leave a third of the CUs idle (us, small and large: int8 1000 x
+// 1500 x 777 12.2 and 14.8, its dW 20 and 25, dX 26 and 39; the gated form of 192
+// tiles 22 and 19; 2047^3 int8 37 and 26, dX 113 and 93).
 template <Form F, Elem E, Elem OUT>
 hipError_t launch_form(const LayerArgs& a, hipStream_t s) {
     using Wide = Tile<F, E, OUT, 256, 256, 128, 128, 4>;
@@ -225,8 +226,9 @@ hipError_t launch_form(const LayerArgs& a, hipStream_t s) {
     };
     if (!big_fits<Mid>(a)) {
         using Small = Tile<F, E, OUT, 64, G ? 128 : 64, 32, G ? 64 : 32>;
-        if (tiles(Mid{}) <= a.cus) return launch_tiles<Small>(tile_kernel<Small>, a, s);
-        return launch_tiles<Mid>(tile_kernel<Mid>, a, s);
+        if (!rows_of_16<Mid>(a)) return launch_tiles<Small>(tile_kernel<Small, true>, a, s);
+        if (3 * tiles(Mid{}) <= 2ll * a.cus) return launch_tiles<Small>(tile_kernel<Small, false>, a, s);
+        return launch_tiles<Mid>(tile_kernel<Mid, false>, a, s);
     }
     using S32 = Tile<F, E, OUT, 32, 64, 32, 64>;
     using S64 = Tile<F, E, OUT, 64, 64, 64, 64>;

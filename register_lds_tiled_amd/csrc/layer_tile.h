@@ -217,13 +217,20 @@ __device__ __forceinline__ void gated_row(int r, int& m, int& row) {
 }
 
 // Tiles through registers: any alignment, pitch and length.  128 bytes of k at a
-// time, in two LDS places: the next ones are loaded while one multiplies, and
-// written to the other place behind it, so there is one barrier to 128 bytes.
-template <class T>
+// time, in two LDS places: while one multiplies the next AHEAD are on their way,
+// and one is written to the other place behind it, so there is one barrier to 128
+// bytes.  Latency bounds such launches, so the loads are without branches: a chunk
+// that would pass its row's end is the row's last 16 bytes, a k row past K the
+// last one, and what that brings is moved down or cleared when it is written to
+// LDS.  (With the row's end looked after at the load, every load waits for all
+// others: dX of 1000 x 1500 x 777 39 us.)  TINY: rows of less than 16 bytes,
+// loaded by bytes.
+template <class T, bool TINY>
 __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m, int tiles_n) {
     constexpr int BM = T::BM, BN = T::BN, NT = T::NT, FM = T::FM, FN = T::FN, KST = 2 * T::KST;
     constexpr int CA = BM * 8 / NT, CB = BN * 8 / NT;             // a thread's chunks
     static_assert(CA * NT == BM * 8 && CB * NT == BN * 8, "whole rounds of the loader");
+    constexpr int AHEAD = CA + CB <= 6 ? 3 : 2;
     constexpr int STAGE = 2 * (T::SA + T::SB), ROOM = 2 * STAGE > T::EPI ? 2 * STAGE : T::EPI;
     __shared__ __attribute__((aligned(16))) unsigned char lds[ROOM];
     const int per = tiles_m * tiles_n;
@@ -235,88 +242,115 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
     const int wm = (wave / T::WAVES_N) * T::WM, wn = (wave % T::WAVES_N) * T::WN;
     const int li = lane & 31, g = lane >> 5;
     const long long m0 = (long long)tm * BM, n0 = (long long)tn * T::COLS;
-    const long long row_bytes = (long long)p.K * T::ES;
+    const unsigned row_bytes = (unsigned)p.K * T::ES;             // K <= 2^31 - 1
     const int each = (int)(((long long)p.K + KST - 1) / KST), stages = each * T::PAIRS;
-    // Stages of whole k, in tiles whose columns across are whole: plain loads.
-    const int whole = (!T::A_ACROSS || m0 + BM <= p.M) && (!T::B_ACROSS || n0 + BN <= p.N) ? p.K / KST : 0;
 
-    // The thread's chunk u of an operand: its row (or k row) and place in it.  Rows
-    // past a matrix read its last one: their products are not stored.
-    auto along_row = [&](int id) { return id >> 3; };
-    long long arow[CA], brow[CB];           // bytes from the first matrix's start to the row's
+    // The thread's chunk u of an operand.  Along k: a row and 16 bytes of the stage's
+    // 128; rows past a matrix are its last one, their products are not stored.
+    // Across: a k row of the stage and 16 bytes of a row.
+    auto a_row = [&](int u, long long ld) { return min(m0 + ((tid + u * NT) >> 3), (long long)p.M - 1) * ld; };
+    auto across_col = [&](int u, int W, long long first) { return 2 * first + 16 * ((tid + u * NT) % (W / 8)); };
+    auto across_k = [&](int u, int W) { return (tid + u * NT) / (W / 8); };
+    long long arow[CA], brow[CB];           // bytes to the chunk's row, across to its columns
 #pragma unroll
-    for (int u = 0; u < CA; ++u) {
-        const int id = tid + u * NT;
-        arow[u] = T::A_ACROSS ? 2 * m0 : min(m0 + along_row(id), (long long)p.M - 1) * p.lda[0];
-    }
+    for (int u = 0; u < CA; ++u)
+        arow[u] = T::A_ACROSS ? min(across_col(u, BM, m0), 2ll * p.M - (TINY ? 0 : 16)) : a_row(u, p.lda[0]);
 #pragma unroll
     for (int u = 0; u < CB; ++u) {
-        const int id = tid + u * NT;
-        int m = 0, row = along_row(id);
+        int m = 0, row = (tid + u * NT) >> 3;
         if constexpr (T::GATED) gated_row<T>(row, m, row);
-        brow[u] = T::B_ACROSS ? 2 * n0
-                              : (m ? p.B[1] - p.B[0] : 0) + min(n0 + row, (long long)p.N - 1) * (m ? p.ldb[1] : p.ldb[0]);
+        if constexpr (T::B_ACROSS)
+            brow[u] = min(across_col(u, BN, n0), 2ll * p.N - (TINY ? 0 : 16));
+        else
+            brow[u] = (m ? p.B[1] - p.B[0] : 0) + min(n0 + row, (long long)p.N - 1) * (m ? p.ldb[1] : p.ldb[0]);
     }
-    uint4 va[CA], vb[CB];
-    auto fetch = [&](int s) __attribute__((always_inline)) {
+    // Columns past the matrix: chunks to be moved down.
+    const bool a_edge = T::A_ACROSS && m0 + BM > p.M, b_edge = T::B_ACROSS && n0 + BN > p.N;
+    uint4 wait_a[AHEAD][CA], wait_b[AHEAD][CB];
+    auto fetch = [&](int s, auto slot) __attribute__((always_inline)) {
+        uint4(&va)[CA] = wait_a[slot];
+        uint4(&vb)[CB] = wait_b[slot];
         const int pair = T::PAIRS == 2 && s >= each ? 1 : 0;
-        const int st = s - pair * each;
+        const int k0 = (s - pair * each) * KST;
         const int ma = T::OUTS == 2 ? out : pair;
         const unsigned char *const A = p.A[ma], *const B = p.B[pair];
-        const long long lda = p.lda[ma], ldb = p.ldb[pair], k0 = (long long)st * KST;
-        auto a_row = [&](int u) __attribute__((always_inline)) {
-            if constexpr (T::A_ACROSS || T::PAIRS == 1) return arow[u];
-            return min(m0 + along_row(tid + u * NT), (long long)p.M - 1) * lda;
+        const long long lda = p.lda[ma], ldb = p.ldb[pair];
+        auto along = [&](const unsigned char* row, int u) __attribute__((always_inline)) {
+            const unsigned at = (unsigned)k0 * T::ES + 16u * ((tid + u * NT) & 7);
+            if constexpr (TINY) return mx_bytes16(row, at, row_bytes);
+            uint4 v;
+            __builtin_memcpy(&v, row + min(at, row_bytes - 16), 16);
+            return v;
         };
-        auto load = [&](auto plain) __attribute__((always_inline)) {
-            auto get = [&](const unsigned char* row, long long at, long long len) __attribute__((always_inline)) {
-                if constexpr (plain) {
-                    uint4 v;
-                    __builtin_memcpy(&v, row + at, 16);
-                    return v;
-                } else {
-                    return mx_bytes16(row, at, len);
-                }
-            };
-#pragma unroll
-            for (int u = 0; u < CA; ++u) {
-                const int id = tid + u * NT;
-                if constexpr (T::A_ACROSS) {
-                    const long long k = k0 + id / (BM / 8);
-                    va[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (plain || k < p.K) va[u] = get(A + k * lda, 2 * m0 + 16 * (id % (BM / 8)), 2ll * p.M);
-                } else {
-                    va[u] = get(A + a_row(u), k0 * T::ES + 16 * (id & 7), row_bytes);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < CB; ++u) {
-                const int id = tid + u * NT;
-                if constexpr (T::B_ACROSS) {
-                    const long long k = k0 + id / (BN / 8);
-                    vb[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (plain || k < p.K) vb[u] = get(B + k * ldb, 2 * n0 + 16 * (id % (BN / 8)), 2ll * p.N);
-                } else {
-                    vb[u] = get(B + brow[u], k0 * T::ES + 16 * (id & 7), row_bytes);
-                }
-            }
+        auto across = [&](const unsigned char* M, long long ld, int k, long long col, int cols) __attribute__((always_inline)) {
+            const unsigned char* const row = M + min(k0 + k, p.K - 1) * ld;
+            if constexpr (TINY) return mx_bytes16(row, col, 2ll * cols);
+            uint4 v;
+            __builtin_memcpy(&v, row + col, 16);
+            return v;
         };
-        if (st < whole)
-            load(std::true_type{});
-        else
-            load(std::false_type{});
+#pragma unroll
+        for (int u = 0; u < CA; ++u) {
+            if constexpr (T::A_ACROSS)
+                va[u] = across(A, lda, across_k(u, BM), arow[u], p.M);
+            else
+                va[u] = along(A + (T::PAIRS == 2 ? a_row(u, lda) : arow[u]), u);
+        }
+#pragma unroll
+        for (int u = 0; u < CB; ++u) {
+            if constexpr (T::B_ACROSS)
+                vb[u] = across(B, ldb, across_k(u, BN), brow[u], p.N);
+            else
+                vb[u] = along(B + brow[u], u);
+        }
     };
-    auto place = [&](int buf) __attribute__((always_inline)) {
-        unsigned char* const to = lds + buf * STAGE;
+    auto place = [&](int s, auto slot) __attribute__((always_inline)) {
+        unsigned char* const to = lds + (s & 1) * STAGE;
+        const int st = T::PAIRS == 2 && s >= each ? s - each : s;
+        const int left = p.K - st * KST;   // k of the stage
         auto put = [](unsigned char* at, uint4 v) {
             lds_poison_f4(at);
             *reinterpret_cast<uint4*>(at) = v;
+        };
+        // v without its first n bytes, zeros behind them
+        auto down = [](uint4 v, unsigned n) {
+            const uint4 d = mx_down(v, (int)min(max(n, 1u), 16u));
+            return n == 0 ? v : d;
         };
         // 64 bytes of k behind the others
         auto along = [](int id, int S) { return (id >> 2 & 1) * S + (id >> 3) * 64 + 16 * ((id & 3) ^ chunk_at(id >> 3)); };
         auto across = [](int id, auto W) {
             return id / (W / 8) * (2 * W) + 16 * (id % (W / 8) ^ across_swap<W>(id / (W / 8)));
         };
+        // The last stage, and tiles at the edge: what the loads brought from elsewhere.
+        auto along_end = [&](uint4& v, int u) __attribute__((always_inline)) {
+            const unsigned at = (unsigned)st * 128u + 16u * ((tid + u * NT) & 7);
+            if constexpr (!TINY) v = down(v, at - min(at, row_bytes - 16));
+        };
+        auto across_end = [&](uint4& v, int u, int W, long long first, long long col) __attribute__((always_inline)) {
+            if constexpr (!TINY) v = down(v, (unsigned)(across_col(u, W, first) - col));
+            if (across_k(u, W) >= left) v = make_uint4(0u, 0u, 0u, 0u);
+        };
+        uint4(&va)[CA] = wait_a[slot];
+        uint4(&vb)[CB] = wait_b[slot];
+        if (left < KST || a_edge) {
+#pragma unroll
+            for (int u = 0; u < CA; ++u) {
+                if constexpr (T::A_ACROSS)
+                    across_end(va[u], u, BM, m0, arow[u]);
+                else
+                    along_end(va[u], u);
+            }
+        }
+        if (left < KST || b_edge) {
+#pragma unroll
+            for (int u = 0; u < CB; ++u) {
+                if constexpr (T::B_ACROSS)
+                    across_end(vb[u], u, BN, n0, brow[u]);
+                else
+                    along_end(vb[u], u);
+            }
+        }
 #pragma unroll
         for (int u = 0; u < CA; ++u) {
             const int id = tid + u * NT;
@@ -330,14 +364,8 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
     };
 
     acc_of<T::E> acc[FM][FN] = {};
-    if (stages > 0) {
-        fetch(0);
-        place(0);
-    }
-    __syncthreads();
-    for (int s = 0; s < stages; ++s) {
-        if (s + 1 < stages) fetch(s + 1);
-        const unsigned char* const st = lds + (s & 1) * STAGE;
+    auto multiply = [&](int buf) __attribute__((always_inline)) {
+        const unsigned char* const st = lds + buf * STAGE;
         static_for<4>([&](auto h) __attribute__((always_inline)) {
             constexpr int t = h % 2;
             const unsigned char *const sa = st + h / 2 * T::SA, *const sb = st + 2 * T::SA + h / 2 * T::SB;
@@ -361,10 +389,42 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
 #pragma unroll
                 for (int j = 0; j < FN; ++j) acc[i][j] = mfma<T::E>(a[i], b[j], acc[i][j]);
         });
-        if (s + 1 < stages) place((s + 1) & 1);
+    };
+    // Stage s waits in registers at s % AHEAD until it is placed.  Past the last
+    // stage that one is loaded again: the loads stay without branches.
+    constexpr std::integral_constant<int, 0> none{};
+    if (stages > 0) {
+        static_for<AHEAD>([&](auto s) __attribute__((always_inline)) { fetch(min((int)s, stages - 1), s); });
+        place(0, none);
+        fetch(min(AHEAD, stages - 1), none);
         __syncthreads();
+        auto stage = [&](int s, auto d) __attribute__((always_inline)) {
+            constexpr std::integral_constant<int, (d + 1) % AHEAD> next{};
+            multiply(s & 1);
+            if (s + 1 < stages) place(s + 1, next);
+            fetch(min(s + 1 + AHEAD, stages - 1), next);
+            __syncthreads();
+        };
+        int s = 0;
+        for (;;) {
+            stage(s, std::integral_constant<int, 0>{});
+            if (++s == stages) break;
+            stage(s, std::integral_constant<int, 1 % AHEAD>{});
+            if (++s == stages) break;
+            if constexpr (AHEAD == 3) {
+                stage(s, std::integral_constant<int, 2>{});
+                if (++s == stages) break;
+            }
+        }
     }
     epilogue<T>(p, out, acc, reinterpret_cast<float*>(lds), wave, m0 + wm, n0 + (T::GATED ? wn / 2 : wn), lane);
+}
+
+// Whether every row that the kernel above reads has 16 bytes.
+template <class T>
+inline bool rows_of_16(const LayerArgs& a) {
+    const bool along = (long long)a.K * T::ES >= 16;
+    return (T::A_ACROSS ? a.M >= 8 : along) && (T::B_ACROSS ? a.N >= 8 : along);
 }
 
 // One workgroup per tile; more threads than a launch holds are refused by the
