@@ -196,7 +196,7 @@ hipError_t launch_few(const LayerArgs& a, hipStream_t s) {
 
 // Whether a product takes the kernel above: at most 32 rows, or 64 where its rows
 // do not lie on 16 bytes (else tiles whose waves divide k: 64 rows, 8192 x 8192 int8
-// 24.5 us against 28, 4096 x 4096 8.9 against 12); columns that a launch of 512
+// 18.7 us against 28, 4096 x 4096 7.5 against 12); columns that a launch of 512
 // threads per 16 holds; and rows in reach of 32-bit offsets.
 inline bool few_rows(const LayerArgs& a, int size, bool gated) {
     auto whole = [&](const void* p, long long ld) { return mx_aligned(p, ld, 16); };

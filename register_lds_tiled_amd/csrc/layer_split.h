@@ -2,13 +2,15 @@
 // divide k, and the choice of a product's tiles.
 //
 // For products with too few 128 x 128 tiles to fill the CUs (a batch in decoding,
-// a short prompt, narrow layers): a workgroup owns 32 to 64 rows and 64 or 128
-// columns of products, and each of its four waves the whole tile for every fourth
-// stage of 64 bytes of k.  A wave
-// brings its stages by DMA into a ring of its own in LDS, so the loop needs no
-// barrier, and nearly all of LDS is on its way from memory all the time: such
-// launches are bound by what the caches deliver and by its latency.  The waves'
-// parts are added at the end, in wave order, through LDS.
+// a short prompt, narrow layers): a workgroup owns 32 or 64 rows and 64 columns of
+// products, and each of its four waves the whole tile for every fourth stage of
+// 128 bytes of k.  A wave brings its stages by DMA into a ring of its own in LDS,
+// and the next into a stage's place as soon as that is in registers, so the loop
+// needs no barrier, and nearly all of LDS is on its way from memory all the time:
+// such launches are bound by what the caches deliver and by its latency.  Stages
+// are whole cache lines because a request for a line that is still on its way
+// stalls the ones behind it (with 64 bytes int8 128 x 4096 x 4096 took 11.9 us, 9.6
+// so).  The waves' parts are added at the end, in wave order, through LDS.
 #pragma once
 
 #include "layer_big.h"
@@ -28,9 +30,9 @@ __device__ __forceinline__ void wait_loads() {
 // T: the tile with one wave to all of it (WM = BM, WN = BN).
 template <class T, int RING>
 __global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int tiles_m, int tiles_n) {
-    constexpr int BM = T::BM, BN = T::BN, FM = T::FM, FN = T::FN, KST = T::KST, ES = T::ES;
-    constexpr int STAGE = T::SA + T::SB, MINE = RING * STAGE;
-    constexpr int AQ = T::SA / 1024, BQ = T::SB / 1024, NDMA = AQ + BQ;
+    constexpr int BM = T::BM, BN = T::BN, FM = T::FM, FN = T::FN, KST = 2 * T::KST, ES = T::ES;
+    constexpr int A_BYTES = 2 * T::SA, B_BYTES = 2 * T::SB, STAGE = A_BYTES + B_BYTES, MINE = RING * STAGE;
+    constexpr int AQ = A_BYTES / 1024, BQ = B_BYTES / 1024, NDMA = AQ + BQ;
     constexpr int PART = BM * T::STR * 4;
     static_assert(T::NW == 1 && PART <= MINE, "a wave's part of the result in its ring");
     __shared__ __attribute__((aligned(1024))) unsigned char lds[kSplit * MINE];
@@ -51,7 +53,7 @@ __global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int til
     const int pad = (int)((long long)each * KST - p.K);
     const int mine = (nst - wave + kSplit - 1) / kSplit;   // this wave's
     auto along = [&](int v, int row, long long ld, int& kk) __attribute__((always_inline)) {
-        const int c = (lane & 3) ^ chunk_at(16 * v + (lane >> 2));
+        const int c = (lane & 7) ^ line_at(8 * v + (lane >> 3));
         kk = 16 / ES * c;
         return (unsigned)row * (unsigned)ld + 16u * (unsigned)c;
     };
@@ -70,7 +72,7 @@ __global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int til
         if constexpr (T::A_ACROSS)
             aoff[u] = across(u, std::integral_constant<int, BM>{}, mlast, p.lda[pa], akk[u]);
         else
-            aoff[u] = along(u, min(16 * u + (lane >> 2), mlast), p.lda[pa], akk[u]);
+            aoff[u] = along(u, min(8 * u + (lane >> 3), mlast), p.lda[pa], akk[u]);
     }
 #pragma unroll
     for (int u = 0; u < BQ; ++u) {
@@ -78,10 +80,10 @@ __global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int til
             bbase[u] = p.B[0] + 2 * n0;
             boff[u] = across(u, std::integral_constant<int, BN>{}, nlast, p.ldb[0], bkk[u]);
         } else {
-            int m = 0, row = 16 * u;
+            int m = 0, row = 8 * u;
             if constexpr (T::GATED) gated_row<T>(row, m, row);
             bbase[u] = p.B[m] + n0 * p.ldb[m];
-            boff[u] = along(u, min(row + (lane >> 2), nlast), p.ldb[m], bkk[u]);
+            boff[u] = along(u, min(row + (lane >> 3), nlast), p.ldb[m], bkk[u]);
         }
     }
     // Stage i of this wave into its place of the ring.
@@ -100,33 +102,34 @@ __global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int til
 #pragma unroll
             for (int u = 0; u < BQ; ++u)
                 lds_dma16(bkk[u] >= pad ? bbase[u] + b + boff[u] : zero,
-                          __builtin_amdgcn_readfirstlane(to + T::SA + 1024u * u));
+                          __builtin_amdgcn_readfirstlane(to + A_BYTES + 1024u * u));
         } else {
 #pragma unroll
             for (int u = 0; u < AQ; ++u) lds_dma16s(a, aoff[u], __builtin_amdgcn_readfirstlane(to + 1024u * u));
 #pragma unroll
             for (int u = 0; u < BQ; ++u)
-                lds_dma16s(bbase[u] + b, boff[u], __builtin_amdgcn_readfirstlane(to + T::SA + 1024u * u));
+                lds_dma16s(bbase[u] + b, boff[u], __builtin_amdgcn_readfirstlane(to + A_BYTES + 1024u * u));
         }
     };
-    uint4 a[2][FM], b[2][FN];
+    uint4 a[4][FM], b[4][FN];
     auto read = [&](int i) __attribute__((always_inline)) {
         const unsigned char* const st = lds + wave * MINE + i % RING * STAGE;
+        auto line = [&](int r, int h) { return (r + li) * 128 + 16 * ((4 * g + h) ^ line_at(li)); };
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int h = 0; h < 4; ++h) {
 #pragma unroll
             for (int j = 0; j < FM; ++j) {
                 if constexpr (T::A_ACROSS)
-                    a[t][j] = read_across<BM>(st + across_at<BM>(0, j, t, lane));
+                    a[h][j] = read_across<BM>(st + across_at<BM, 32>(0, j, h, lane));
                 else
-                    a[t][j] = *reinterpret_cast<const uint4*>(st + along_at(0, j, t, li, g));
+                    a[h][j] = *reinterpret_cast<const uint4*>(st + line(32 * j, h));
             }
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 if constexpr (T::B_ACROSS)
-                    b[t][j] = read_across<BN>(st + T::SA + across_at<BN>(0, j, t, lane));
+                    b[h][j] = read_across<BN>(st + A_BYTES + across_at<BN, 32>(0, j, h, lane));
                 else
-                    b[t][j] = *reinterpret_cast<const uint4*>(st + T::SA + along_at(0, j, t, li, g));
+                    b[h][j] = *reinterpret_cast<const uint4*>(st + A_BYTES + line(32 * j, h));
             }
         }
         // the stage is in registers: its place is free
@@ -136,11 +139,11 @@ __global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int til
     acc_of<T::E> acc[FM][FN] = {};
     auto multiply = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int h = 0; h < 4; ++h)
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = mfma<T::E>(a[t][i], b[t][j], acc[i][j]);
+                for (int j = 0; j < FN; ++j) acc[i][j] = mfma<T::E>(a[h][i], b[h][j], acc[i][j]);
     };
 #pragma unroll
     for (int i = 0; i < RING; ++i)
@@ -150,6 +153,7 @@ __global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int til
         wait_loads<(RING - 1) * NDMA>();
         read(i);
         request(i + RING);
+        __builtin_amdgcn_sched_barrier(0);
         multiply();
     }
     wait_loads<0>();
@@ -205,12 +209,14 @@ hipError_t launch_split(const LayerArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// A product's tiles.  Of those whose waves divide k the smallest that fits one
-// round of workgroups, one to a CU; else 128 x 128 up to two to a CU, and 256 x
-// 256 beyond.  us, K = 4096 (the next larger choice in brackets): int8 64 x 4096
-// 8.9 (12.6), 128 x 4096 11.9 (17.4), 512 x 4096 19.5 (21.1), 1024 x 4096 23.5
-// (48.9); gated bf16 64 x 4096 25 (34), 128 x 4096 31 (43), 512 x 2048 34 (47), 1024
-// x 4096 73 (92), 1024 x 8192 147 and 111; dX 512 x 4096 59 (99).
+// A product's tiles.  32 x 64 or 64 x 64 with divided k where they fit one round of
+// workgroups, one to a CU, the latter also two rounds of them (but for a single
+// row of tiles, which memory bounds: gated bf16 64 x 16384 x 4096 88 us, 65 in 128 x
+// 128); else 128 x 128 up to two to a CU, and 256 x 256 beyond.  us, K = 4096 (the
+// next larger choice in brackets): int8 64 x 4096 7.5 (9.6), 128 x 4096 9.6 (22),
+// 512 x 4096 19 (22), 1024 x 4096 23 (49); gated bf16 64 x 4096 19 (24), 128 x 4096 23
+// (54), 512 x 2048 35 (51), 1024 x 4096 73 (92), 1024 x 8192 147 and 111; dX 512 x 4096
+// 69 (100).
 // Rows off 16 bytes go through registers, in 64 x 64 (gated: x 128) products where
 // 128 x 128 would leave a third of the CUs idle (us, small and large: int8 1000 x
 // 1500 x 777 12.2 and 14.8, its dW 20 and 25, dX 26 and 39; the gated form of 192
@@ -232,10 +238,8 @@ hipError_t launch_form(const LayerArgs& a, hipStream_t s) {
     }
     using S32 = Tile<F, E, OUT, 32, 64, 32, 64>;
     using S64 = Tile<F, E, OUT, 64, 64, 64, 64>;
-    using S128 = Tile<F, E, OUT, 64, 128, 64, 128>;
-    if (tiles(S32{}) <= a.cus) return launch_split<S32, 3>(a, s);
-    if (tiles(S64{}) <= a.cus) return launch_split<S64, 3>(a, s);
-    if (tiles(S128{}) <= a.cus) return launch_split<S128, 3>(a, s);
+    if (tiles(S32{}) <= a.cus) return launch_split<S32, 2>(a, s);
+    if (tiles(S64{}) <= (a.M > 64 ? 2ll : 1ll) * a.cus) return launch_split<S64, 2>(a, s);
     if (tiles(Mid{}) <= 2ll * a.cus) return launch_tiles<Mid>(big_kernel<Mid>, a, s);
     return launch_tiles<Wide>(big_kernel<Wide>, a, s);
 }

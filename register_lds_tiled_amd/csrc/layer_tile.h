@@ -400,9 +400,9 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
         __syncthreads();
         auto stage = [&](int s, auto d) __attribute__((always_inline)) {
             constexpr std::integral_constant<int, (d + 1) % AHEAD> next{};
-            multiply(s & 1);
-            if (s + 1 < stages) place(s + 1, next);
+            if (s + 1 < stages) place(s + 1, next);   // where stage s - 1 was read
             fetch(min(s + 1 + AHEAD, stages - 1), next);
+            multiply(s & 1);
             __syncthreads();
         };
         int s = 0;
