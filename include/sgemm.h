@@ -444,6 +444,7 @@ SGEMM_API int gemm_gated_f16(int M, int N, int K, const void *X, int ldx,
  *   not computed and neither they nor X are looked at (one of the two ->
  *   SGEMM_EINVAL_PTR).  Results overwrite.
  * - M == 0 sets DWG and DWU to zero, N == 0 sets DX to zero.
+ * - Of SGEMM_EINVAL_DIM's threads of one launch, DWG and DWU together count.
  * Up to three launches, in stream order.
  */
 SGEMM_API int gemm_gated_backward_bf16(int M, int N, int K, const void *X, int ldx,

@@ -300,16 +300,21 @@ def _mx_kinds():
 
 
 _torch = None
+_tensor = ()
 _raw_stream = None
+_current_device = None
+_functions = {}
 
 
 def _mx_setup():
-    """torch, and its call for the current stream's handle on a device."""
-    global _torch, _raw_stream
+    """torch, and its calls for the current device and its stream's handle."""
+    global _torch, _tensor, _raw_stream, _current_device
     import torch
     _mx_kinds()
     _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
                    or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _tensor = torch.Tensor
     _torch = torch
 
 
@@ -321,49 +326,53 @@ def _no_c_int(name, n):
 def _mx_call(name, head, operands, stream, check, tail=()):
     """One entry point of the MXFP4, 8-bit integer and gated families: `head` its
     leading integers, `operands` (kind, address or tensor or None, leading
-    dimension; "vector" has none) in the C order, `tail` the integers behind
-    them, all of them within a C int's range.  Tensors lie on one device, whose
-    current stream is the default and which is the current device during the
-    call."""
+    dimension) in the C order, `tail` the integers behind them, all of them
+    within a C int's range; of kind "vector" the third is how many neighbouring
+    values a tensor has at least, and is not passed.  Tensors lie on one device,
+    whose current stream is the default and which is the current device during
+    the call."""
     if _torch is None:
         _mx_setup()
-    tensor = _torch.Tensor
-    args, dev = list(head), None
+    args, dev, bits = list(head), -2, 0
     for n in head:
-        if not -0x80000000 <= n <= 0x7FFFFFFF:
-            _no_c_int(name, n)
+        bits |= n
     for kind, x, ld in operands:
-        if not -0x80000000 <= ld <= 0x7FFFFFFF:
-            _no_c_int(name, ld)
-        if isinstance(x, tensor):
+        if isinstance(x, _tensor):
             if x.dtype not in _MX_KINDS[kind]:
                 raise TypeError(f"{name}: a {kind} operand cannot be a {x.dtype} tensor")
-            if not x.is_cuda:
-                raise ValueError("matrix tensors must live on the GPU")
             at = x.get_device()
-            if dev is None:
+            if at != dev:
+                if at < 0:
+                    raise ValueError("matrix tensors must live on the GPU")
+                if dev >= 0:
+                    raise ValueError(f"{name}: operands on devices {dev} and {at}")
                 dev = at
-            elif dev != at:
-                raise ValueError(f"{name}: operands on devices {dev} and {at}")
-            x = x.data_ptr() or None
-        elif x is not None:
-            x = _ptr(x)
-        args.append(x)
+            if kind == "vector" and (x.numel() < ld or not x.is_contiguous()):
+                raise ValueError(f"{name}: {ld} scales are {ld} neighbouring floats")
+            args.append(x.data_ptr())
+        else:
+            args.append(x if x is None else _ptr(x))
         if kind != "vector":
+            bits |= ld
             args.append(ld)
     for n in tail:
-        if not -0x80000000 <= n <= 0x7FFFFFFF:
-            _no_c_int(name, n)
+        bits |= n
         args.append(n)
-    fn = getattr(_lib or library(), name)
-    if dev is not None and dev != _torch.cuda.current_device():
-        with _torch.cuda.device(dev):
-            st = fn(*args, (_raw_stream(dev) or None) if stream is None else _stream(stream))
-    elif dev is not None and stream is None:
-        st = fn(*args, _raw_stream(dev) or None)
-    else:
+    if bits >> 31:   # a negative number, or one of more than 31 bits
+        for n in (*head, *(o[2] for o in operands if o[0] != "vector"), *tail):
+            if not -0x80000000 <= n <= 0x7FFFFFFF:
+                _no_c_int(name, n)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(library(), name)
+    if dev < 0:
         st = fn(*args, _stream(stream))
-    return _check(st) if check else st
+    elif dev == _current_device():
+        st = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    else:
+        with _torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    return _check(st) if check and st else st
 
 
 def _mx_quantize(t, R, C, X, ldx, Q, ldq, S, lds, QT, ldqt, ST, ldst, stream, check):
@@ -443,105 +452,96 @@ def gemm_f16_mxfp4_f32(M, N, K, A, lda, B, ldb, SB, ldsb, C, ldc, stream=None, *
 
 # ---- 8-bit integers with a scale per row, and the gated feed-forward block --
 
-def _vector(name, x, n):
-    """A scales operand: a tensor of `n` neighbouring floats, or an address."""
-    if hasattr(x, "numel") and (x.numel() < n or not x.is_contiguous()):
-        raise ValueError(f"{name}: {n} scales are {n} neighbouring floats")
-    return "vector", x, 0
-
-
 def _act(act):
     return GATED_ACTS[act] if isinstance(act, str) else int(act)
 
 
-def _i8_quantize(t, R, C, X, ldx, Q, ldq, S, stream, check):
-    name = f"gemm_i8_quantize_{t}"
-    return _mx_call(name, (R, C), ((t, X, ldx), ("i8", Q, ldq), _vector(name, S, R)), stream, check)
+def _i8_quantize(name, t, R, C, X, ldx, Q, ldq, S, stream, check):
+    return _mx_call(name, (R, C), ((t, X, ldx), ("i8", Q, ldq), ("vector", S, R)), stream, check)
 
 
 def gemm_i8_quantize_f32(R, C, X, ldx, Q, ldq, S, stream=None, *, check=True) -> int:
     """X (R x C, float32) to whole numbers Q (int8) with a scale per row S (R
     neighbouring float32): X is Q * S[:, None], each off by half a scale at most."""
-    return _i8_quantize("f32", R, C, X, ldx, Q, ldq, S, stream, check)
+    return _i8_quantize("gemm_i8_quantize_f32", "f32", R, C, X, ldx, Q, ldq, S, stream, check)
 
 
 def gemm_i8_quantize_bf16(R, C, X, ldx, Q, ldq, S, stream=None, *, check=True) -> int:
     """gemm_i8_quantize_f32 for bfloat16 X."""
-    return _i8_quantize("bf16", R, C, X, ldx, Q, ldq, S, stream, check)
+    return _i8_quantize("gemm_i8_quantize_bf16", "bf16", R, C, X, ldx, Q, ldq, S, stream, check)
 
 
 def gemm_i8_quantize_f16(R, C, X, ldx, Q, ldq, S, stream=None, *, check=True) -> int:
     """gemm_i8_quantize_f32 for binary16 X."""
-    return _i8_quantize("f16", R, C, X, ldx, Q, ldq, S, stream, check)
+    return _i8_quantize("gemm_i8_quantize_f16", "f16", R, C, X, ldx, Q, ldq, S, stream, check)
 
 
-def _i8_dequantize(t, R, C, Q, ldq, S, Y, ldy, stream, check):
-    name = f"gemm_i8_dequantize_{t}"
-    return _mx_call(name, (R, C), (("i8", Q, ldq), _vector(name, S, R), (t, Y, ldy)), stream, check)
+def _i8_dequantize(name, t, R, C, Q, ldq, S, Y, ldy, stream, check):
+    return _mx_call(name, (R, C), (("i8", Q, ldq), ("vector", S, R), (t, Y, ldy)), stream, check)
 
 
 def gemm_i8_dequantize_f32(R, C, Q, ldq, S, Y, ldy, stream=None, *, check=True) -> int:
     """Y (R x C, float32) = Q * S[:, None]."""
-    return _i8_dequantize("f32", R, C, Q, ldq, S, Y, ldy, stream, check)
+    return _i8_dequantize("gemm_i8_dequantize_f32", "f32", R, C, Q, ldq, S, Y, ldy, stream, check)
 
 
 def gemm_i8_dequantize_bf16(R, C, Q, ldq, S, Y, ldy, stream=None, *, check=True) -> int:
     """gemm_i8_dequantize_f32 into bfloat16 Y."""
-    return _i8_dequantize("bf16", R, C, Q, ldq, S, Y, ldy, stream, check)
+    return _i8_dequantize("gemm_i8_dequantize_bf16", "bf16", R, C, Q, ldq, S, Y, ldy, stream, check)
 
 
 def gemm_i8_dequantize_f16(R, C, Q, ldq, S, Y, ldy, stream=None, *, check=True) -> int:
     """gemm_i8_dequantize_f32 into binary16 Y."""
-    return _i8_dequantize("f16", R, C, Q, ldq, S, Y, ldy, stream, check)
+    return _i8_dequantize("gemm_i8_dequantize_f16", "f16", R, C, Q, ldq, S, Y, ldy, stream, check)
 
 
-def _i8_product(t, M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check):
-    name = f"gemm_i8_{t}"
-    return _mx_call(name, (M, N, K), (("i8", A, lda), _vector(name, SA, M), ("i8", B, ldb),
-                                      _vector(name, SB, N), (t, C, ldc)), stream, check)
+def _i8_product(name, t, M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check):
+    return _mx_call(name, (M, N, K), (("i8", A, lda), ("vector", SA, M), ("i8", B, ldb),
+                                      ("vector", SB, N), (t, C, ldc)), stream, check)
 
 
 def gemm_i8_f32(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream=None, *, check=True) -> int:
     """C = (A.B^T) * SA[:, None] * SB, A (M x K) and B (N x K) int8, the sums
     exact, float32 C."""
-    return _i8_product("f32", M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check)
+    return _i8_product("gemm_i8_f32", "f32", M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check)
 
 
 def gemm_i8_bf16(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream=None, *, check=True) -> int:
     """gemm_i8_f32 with C rounded to bfloat16."""
-    return _i8_product("bf16", M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check)
+    return _i8_product("gemm_i8_bf16", "bf16", M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream,
+                       check)
 
 
 def gemm_i8_f16(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream=None, *, check=True) -> int:
     """gemm_i8_f32 with C rounded to binary16."""
-    return _i8_product("f16", M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check)
+    return _i8_product("gemm_i8_f16", "f16", M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check)
 
 
-def _i8_gated(t, M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh, act, stream, check):
-    name = f"gemm_i8_gated_{t}"
-    return _mx_call(name, (M, N, K), (("i8", A, lda), _vector(name, SA, M), ("i8", BG, ldbg),
-                                      _vector(name, SBG, N), ("i8", BU, ldbu),
-                                      _vector(name, SBU, N), (t, H, ldh)), stream, check,
-                    (_act(act),))
+def _i8_gated(name, t, M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh, act, stream,
+              check):
+    return _mx_call(name, (M, N, K), (("i8", A, lda), ("vector", SA, M), ("i8", BG, ldbg),
+                                      ("vector", SBG, N), ("i8", BU, ldbu), ("vector", SBU, N),
+                                      (t, H, ldh)), stream, check, (_act(act),))
 
 
 def gemm_i8_gated_bf16(M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh,
                        act=ACT_SILU, stream=None, *, check=True) -> int:
     """H = act(g) * u with g and u the products gemm_i8_f32 makes of A with BG and
     BU, H (M x N) bfloat16; act is an int or a name in GATED_ACTS."""
-    return _i8_gated("bf16", M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh, act,
-                     stream, check)
+    return _i8_gated("gemm_i8_gated_bf16", "bf16", M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU,
+                     H, ldh, act, stream, check)
 
 
 def gemm_i8_gated_f16(M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh,
                       act=ACT_SILU, stream=None, *, check=True) -> int:
     """gemm_i8_gated_bf16 into binary16 H."""
-    return _i8_gated("f16", M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh, act,
-                     stream, check)
+    return _i8_gated("gemm_i8_gated_f16", "f16", M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU,
+                     H, ldh, act, stream, check)
 
 
-def _gated(t, M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh, act, stream, check):
-    return _mx_call(f"gemm_gated_{t}", (M, N, K),
+def _gated(name, t, M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh, act, stream,
+           check):
+    return _mx_call(name, (M, N, K),
                     ((t, X, ldx), (t, WG, ldwg), (t, WU, ldwu), (t, G, ldg), (t, U, ldu),
                      (t, H, ldh)), stream, check, (_act(act),))
 
@@ -550,21 +550,21 @@ def gemm_gated_bf16(M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh,
                     stream=None, *, check=True) -> int:
     """H = act(X.WG^T) * (X.WU^T), X (M x K), WG and WU (N x K), H (M x N) bfloat16;
     G and U, both or neither None, receive the two products."""
-    return _gated("bf16", M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh, act,
-                  stream, check)
+    return _gated("gemm_gated_bf16", "bf16", M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu,
+                  H, ldh, act, stream, check)
 
 
 def gemm_gated_f16(M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh, act=ACT_SILU,
                    stream=None, *, check=True) -> int:
     """gemm_gated_bf16 in binary16."""
-    return _gated("f16", M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh, act,
-                  stream, check)
+    return _gated("gemm_gated_f16", "f16", M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu,
+                  H, ldh, act, stream, check)
 
 
-def _gated_backward(t, M, N, K, operands, act, stream, check):
+def _gated_backward(name, t, M, N, K, operands, act, stream, check):
     it = iter(operands)
-    return _mx_call(f"gemm_gated_backward_{t}", (M, N, K), [(t, x, ld) for x, ld in zip(it, it)],
-                    stream, check, (_act(act),))
+    return _mx_call(name, (M, N, K), [(t, x, ld) for x, ld in zip(it, it)], stream, check,
+                    (_act(act),))
 
 
 def gemm_gated_backward_bf16(M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, DH, lddh,
@@ -572,18 +572,18 @@ def gemm_gated_backward_bf16(M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu
                              act=ACT_SILU, stream=None, *, check=True) -> int:
     """The gradients of gemm_gated_bf16 from DH: DG and DU (M x N), DX (M x K, or
     None), DWG and DWU (N x K, or both None)."""
-    return _gated_backward("bf16", M, N, K, (X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, DH, lddh,
-                                             DG, lddg, DU, lddu, DX, lddx, DWG, lddwg, DWU, lddwu),
-                           act, stream, check)
+    return _gated_backward("gemm_gated_backward_bf16", "bf16", M, N, K,
+                           (X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, DH, lddh, DG, lddg,
+                            DU, lddu, DX, lddx, DWG, lddwg, DWU, lddwu), act, stream, check)
 
 
 def gemm_gated_backward_f16(M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, DH, lddh,
                             DG, lddg, DU, lddu, DX, lddx, DWG, lddwg, DWU, lddwu,
                             act=ACT_SILU, stream=None, *, check=True) -> int:
     """gemm_gated_backward_bf16 in binary16."""
-    return _gated_backward("f16", M, N, K, (X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, DH, lddh,
-                                            DG, lddg, DU, lddu, DX, lddx, DWG, lddwg, DWU, lddwu),
-                           act, stream, check)
+    return _gated_backward("gemm_gated_backward_f16", "f16", M, N, K,
+                           (X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, DH, lddh, DG, lddg,
+                            DU, lddu, DX, lddx, DWG, lddwg, DWU, lddwu), act, stream, check)
 
 
 def matmul(A, B, out=None, path=PATH_AUTO, stream=None):

@@ -13,10 +13,10 @@ constexpr int kMostK = 131071;   // of 8-bit products: 131071 * 128 * 128 < 2^31
 
 bool act_known(int act) { return act >= SGEMM_ACT_NONE && act <= SGEMM_ACT_GELU_TANH; }
 
-// 256 threads per 64 x 64 tile of an output fit a launch; no kernel here is
-// launched with more.
-bool launchable(long long rows, long long cols) {
-    return (rows + 63) / 64 * ((cols + 63) / 64) * 256 <= 0xFFFFFFFFll;
+// 256 threads per 64 x 64 tile of an output, or of all outputs of one launch, fit
+// a launch; no kernel here is launched with more.
+bool launchable(long long rows, long long cols, int outputs = 1) {
+    return (rows + 63) / 64 * ((cols + 63) / 64) * outputs * 256 <= 0xFFFFFFFFll;
 }
 
 int quantize(int R, int C, const void* X, int ldx, void* Q, int ldq, float* S, void* stream, Elem t) {
@@ -153,7 +153,7 @@ int gated_backward(int M, int N, int K, const void* X, int ldx, const void* WG, 
         return SGEMM_EINVAL_PTR;
     if (dx && N > 0 && (WG == nullptr || WU == nullptr)) return SGEMM_EINVAL_PTR;
     if (dw && M > 0 && X == nullptr) return SGEMM_EINVAL_PTR;
-    if ((slopes && !launchable(M, N)) || (dx && !launchable(M, K)) || (dw && !launchable(N, K)))
+    if ((slopes && !launchable(M, N)) || (dx && !launchable(M, K)) || (dw && !launchable(N, K, 2)))
         return SGEMM_EINVAL_DIM;
     Ranges g;
     if (slopes) {
