@@ -242,7 +242,7 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
     const int wm = (wave / T::WAVES_N) * T::WM, wn = (wave % T::WAVES_N) * T::WN;
     const int li = lane & 31, g = lane >> 5;
     const long long m0 = (long long)tm * BM, n0 = (long long)tn * T::COLS;
-    const unsigned row_bytes = (unsigned)p.K * T::ES;             // K <= 2^31 - 1
+    const long long row_bytes = (long long)p.K * T::ES;
     const int each = (int)(((long long)p.K + KST - 1) / KST), stages = each * T::PAIRS;
 
     // The thread's chunk u of an operand.  Along k: a row and 16 bytes of the stage's
@@ -264,6 +264,8 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
         else
             brow[u] = (m ? p.B[1] - p.B[0] : 0) + min(n0 + row, (long long)p.N - 1) * (m ? p.ldb[1] : p.ldb[0]);
     }
+    // Where the last whole 16 bytes of a row begin, from k0 on (before it, maybe).
+    auto last_chunk = [&](int k0) { return (int)min(row_bytes - (long long)k0 * T::ES, 1024ll) - 16; };
     // Columns past the matrix: chunks to be moved down.
     const bool a_edge = T::A_ACROSS && m0 + BM > p.M, b_edge = T::B_ACROSS && n0 + BN > p.N;
     uint4 wait_a[AHEAD][CA], wait_b[AHEAD][CB];
@@ -275,15 +277,17 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
         const int ma = T::OUTS == 2 ? out : pair;
         const unsigned char *const A = p.A[ma], *const B = p.B[pair];
         const long long lda = p.lda[ma], ldb = p.ldb[pair];
+        const long long start = (long long)k0 * T::ES;
+        const int end = last_chunk(k0);
         auto along = [&](const unsigned char* row, int u) __attribute__((always_inline)) {
-            const unsigned at = (unsigned)k0 * T::ES + 16u * ((tid + u * NT) & 7);
-            if constexpr (TINY) return mx_bytes16(row, at, row_bytes);
+            const int at = 16 * ((tid + u * NT) & 7);
+            if constexpr (TINY) return mx_bytes16(row, start + at, row_bytes);
             uint4 v;
-            __builtin_memcpy(&v, row + min(at, row_bytes - 16), 16);
+            __builtin_memcpy(&v, row + start + min(at, end), 16);
             return v;
         };
         auto across = [&](const unsigned char* M, long long ld, int k, long long col, int cols) __attribute__((always_inline)) {
-            const unsigned char* const row = M + min(k0 + k, p.K - 1) * ld;
+            const unsigned char* const row = M + min((unsigned)k0 + k, (unsigned)p.K - 1) * ld;
             if constexpr (TINY) return mx_bytes16(row, col, 2ll * cols);
             uint4 v;
             __builtin_memcpy(&v, row + col, 16);
@@ -324,8 +328,8 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
         };
         // The last stage, and tiles at the edge: what the loads brought from elsewhere.
         auto along_end = [&](uint4& v, int u) __attribute__((always_inline)) {
-            const unsigned at = (unsigned)st * 128u + 16u * ((tid + u * NT) & 7);
-            if constexpr (!TINY) v = down(v, at - min(at, row_bytes - 16));
+            const int at = 16 * ((tid + u * NT) & 7);
+            if constexpr (!TINY) v = down(v, (unsigned)(at - min(at, last_chunk(st * KST))));
         };
         auto across_end = [&](uint4& v, int u, int W, long long first, long long col) __attribute__((always_inline)) {
             if constexpr (!TINY) v = down(v, (unsigned)(across_col(u, W, first) - col));
