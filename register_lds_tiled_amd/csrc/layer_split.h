@@ -219,8 +219,12 @@ hipError_t launch_split(const LayerArgs& a, hipStream_t s) {
 // 69 (100).
 // Rows off 16 bytes go through registers, in 64 x 64 (gated: x 128) products where
 // 128 x 128 would leave a third of the CUs idle (us, small and large: int8 1000 x
-// 1500 x 777 12.2 and 14.8, its dW 20 and 25, dX 26 and 39; the gated form of 192
-// tiles 22 and 19; 2047^3 int8 37 and 26, dX 113 and 93).
+// 1500 x 777 12.2 and 14.7, its dW 20 and 22, dX 26 and 34; the gated form of 192
+// tiles 21.5 and 18.9; 2047^3 int8 35 and 25, dX 113 and 75).  The gradients' small
+// tiles have two groups of waves for alternate stages where there are 12 and no
+// more than two workgroups to a CU (us, one group and two: dX 1000 x 777 x 1500 35
+// and 25.5, 70 x 4095 x 4093 91 and 72, of 544 tiles 70.5 and 75; dW 70 x 4095 x
+// 4093 46 and 34, of 768 tiles 20 and 22).  Rows along k gain a tenth at most so.
 template <Form F, Elem E, Elem OUT>
 hipError_t launch_form(const LayerArgs& a, hipStream_t s) {
     using Wide = Tile<F, E, OUT, 256, 256, 128, 128, 4>;
@@ -233,7 +237,12 @@ hipError_t launch_form(const LayerArgs& a, hipStream_t s) {
     if (!big_fits<Mid>(a)) {
         using Small = Tile<F, E, OUT, 64, G ? 128 : 64, 32, G ? 64 : 32>;
         if (!rows_of_16<Mid>(a)) return launch_tiles<Small>(tile_kernel<Small, true>, a, s);
-        if (3 * tiles(Mid{}) <= 2ll * a.cus) return launch_tiles<Small>(tile_kernel<Small, false>, a, s);
+        if (3 * tiles(Mid{}) <= 2ll * a.cus) {
+            if constexpr (Small::B_ACROSS)
+                if (tiles(Small{}) <= 2ll * a.cus && Small::PAIRS * (long long)a.K >= 12 * 2 * Small::KST)
+                    return launch_tiles<Small, 2>(tile_kernel<Small, false, 2>, a, s);
+            return launch_tiles<Small>(tile_kernel<Small, false>, a, s);
+        }
         return launch_tiles<Mid>(tile_kernel<Mid, false>, a, s);
     }
     using S32 = Tile<F, E, OUT, 32, 64, 32, 64>;

@@ -223,24 +223,30 @@ __device__ __forceinline__ void gated_row(int r, int& m, int& row) {
 // that would pass its row's end is the row's last 16 bytes, a k row past K the
 // last one, and what that brings is moved down or cleared when it is written to
 // LDS.  (With the row's end looked after at the load, every load waits for all
-// others: dX of 1000 x 1500 x 777 39 us.)  TINY: rows of less than 16 bytes,
+// others: dX of 1000 x 1500 x 777 39 us.)  Loads off 4 bytes come at 37 KB/us to a
+// CU, on 4 bytes at up to 97: int8 1000 x 1500 x 777 12.2 us, x 780 9.4.  KS groups
+// of waves take every KS-th stage each, in places of their own, and the first adds
+// the others' sums to its own, in their order.  TINY: rows of less than 16 bytes,
 // loaded by bytes.
-template <class T, bool TINY>
-__global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m, int tiles_n) {
+template <class T, bool TINY, int KS = 1>
+__global__ __launch_bounds__(KS * T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m, int tiles_n) {
     constexpr int BM = T::BM, BN = T::BN, NT = T::NT, FM = T::FM, FN = T::FN, KST = 2 * T::KST;
     constexpr int CA = BM * 8 / NT, CB = BN * 8 / NT;             // a thread's chunks
     static_assert(CA * NT == BM * 8 && CB * NT == BN * 8, "whole rounds of the loader");
     constexpr int AHEAD = CA + CB <= 6 ? 3 : 2;
     constexpr int STAGE = 2 * (T::SA + T::SB), ROOM = 2 * STAGE > T::EPI ? 2 * STAGE : T::EPI;
-    __shared__ __attribute__((aligned(16))) unsigned char lds[ROOM];
+    static_assert(NT * FM * FN * 64 <= ROOM, "a group's sums in its places");
+    __shared__ __attribute__((aligned(16))) unsigned char lds[KS * ROOM];
     const int per = tiles_m * tiles_n;
     const int out = T::OUTS == 2 && (int)blockIdx.x >= per ? 1 : 0;
     int tm, tn;
     tile_coords(blockIdx.x - out * per, tiles_m, tiles_n, T::GROUP_M, p.xcds, tm, tn);
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x % NT, lane = tid & 63;
+    const int group = __builtin_amdgcn_readfirstlane((int)threadIdx.x / NT);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = (wave / T::WAVES_N) * T::WM, wn = (wave % T::WAVES_N) * T::WN;
     const int li = lane & 31, g = lane >> 5;
+    unsigned char* const places = lds + group * ROOM;
     const long long m0 = (long long)tm * BM, n0 = (long long)tn * T::COLS;
     const long long row_bytes = (long long)p.K * T::ES;
     const int each = (int)(((long long)p.K + KST - 1) / KST), stages = each * T::PAIRS;
@@ -308,8 +314,8 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
                 vb[u] = along(B + brow[u], u);
         }
     };
-    auto place = [&](int s, auto slot) __attribute__((always_inline)) {
-        unsigned char* const to = lds + (s & 1) * STAGE;
+    auto place = [&](int s, int turn, auto slot) __attribute__((always_inline)) {
+        unsigned char* const to = places + (turn & 1) * STAGE;
         const int st = T::PAIRS == 2 && s >= each ? s - each : s;
         const int left = p.K - st * KST;   // k of the stage
         auto put = [](unsigned char* at, uint4 v) {
@@ -369,7 +375,7 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
 
     acc_of<T::E> acc[FM][FN] = {};
     auto multiply = [&](int buf) __attribute__((always_inline)) {
-        const unsigned char* const st = lds + buf * STAGE;
+        const unsigned char* const st = places + buf * STAGE;
         static_for<4>([&](auto h) __attribute__((always_inline)) {
             constexpr int t = h % 2;
             const unsigned char *const sa = st + h / 2 * T::SA, *const sb = st + 2 * T::SA + h / 2 * T::SB;
@@ -394,32 +400,72 @@ __global__ __launch_bounds__(T::NT, 2) void tile_kernel(LayerArgs p, int tiles_m
                 for (int j = 0; j < FN; ++j) acc[i][j] = mfma<T::E>(a[i], b[j], acc[i][j]);
         });
     };
-    // Stage s waits in registers at s % AHEAD until it is placed.  Past the last
-    // stage that one is loaded again: the loads stay without branches.
+    // The group's turn i is stage KS i + group; it waits in registers at i % AHEAD
+    // until it is placed.  Past the last stage that one is loaded again: the loads
+    // stay without branches.
     constexpr std::integral_constant<int, 0> none{};
     if (stages > 0) {
-        static_for<AHEAD>([&](auto s) __attribute__((always_inline)) { fetch(min((int)s, stages - 1), s); });
-        place(0, none);
-        fetch(min(AHEAD, stages - 1), none);
+        const int turns = (stages + KS - 1) / KS;   // of all groups, for the barriers
+        auto stage_of = [&](int i) { return KS * i + group; };
+        auto bring = [&](int i, auto slot) __attribute__((always_inline)) {
+            fetch(min(stage_of(i), stages - 1), slot);
+        };
+        auto lay = [&](int i, auto slot) __attribute__((always_inline)) {
+            if (stage_of(i) < stages) place(stage_of(i), i, slot);
+        };
+        static_for<AHEAD>([&](auto i) __attribute__((always_inline)) { bring(i, i); });
+        lay(0, none);
+        bring(AHEAD, none);
         __syncthreads();
-        auto stage = [&](int s, auto d) __attribute__((always_inline)) {
+        auto turn = [&](int i, auto d) __attribute__((always_inline)) {
             constexpr std::integral_constant<int, (d + 1) % AHEAD> next{};
-            if (s + 1 < stages) place(s + 1, next);   // where stage s - 1 was read
-            fetch(min(s + 1 + AHEAD, stages - 1), next);
-            multiply(s & 1);
+            lay(i + 1, next);   // where turn i - 1 was read
+            bring(i + 1 + AHEAD, next);
+            if (KS == 1 || stage_of(i) < stages) multiply(i & 1);
             __syncthreads();
         };
-        int s = 0;
+        int i = 0;
         for (;;) {
-            stage(s, std::integral_constant<int, 0>{});
-            if (++s == stages) break;
-            stage(s, std::integral_constant<int, 1 % AHEAD>{});
-            if (++s == stages) break;
+            turn(i, std::integral_constant<int, 0>{});
+            if (++i == turns) break;
+            turn(i, std::integral_constant<int, 1 % AHEAD>{});
+            if (++i == turns) break;
             if constexpr (AHEAD == 3) {
-                stage(s, std::integral_constant<int, 2>{});
-                if (++s == stages) break;
+                turn(i, std::integral_constant<int, 2>{});
+                if (++i == turns) break;
             }
         }
+    }
+    if constexpr (KS > 1) {   // the other groups' sums, in their order
+        auto slot = [&](int of, int q) { return reinterpret_cast<uint4*>(lds + of * ROOM) + q * NT + tid; };
+        if (group > 0) {
+#pragma unroll
+            for (int q = 0; q < FM * FN * 4; ++q) {
+                uint4 v;
+                unsigned w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const auto x = acc[q / 4 / FN][q / 4 % FN][q % 4 * 4 + e];
+                    w[e] = __builtin_bit_cast(unsigned, x);
+                }
+                v = make_uint4(w[0], w[1], w[2], w[3]);
+                *slot(group, q) = v;
+            }
+        }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int of = 1; of < KS; ++of)
+#pragma unroll
+            for (int q = 0; q < FM * FN * 4; ++q) {
+                const uint4 v = *slot(of, q);
+                const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    using V = std::conditional_t<T::E == Elem::i8, int, float>;
+                    acc[q / 4 / FN][q / 4 % FN][q % 4 * 4 + e] += __builtin_bit_cast(V, w[e]);
+                }
+            }
     }
     epilogue<T>(p, out, acc, reinterpret_cast<float*>(lds), wave, m0 + wm, n0 + (T::GATED ? wn / 2 : wn), lane);
 }
@@ -433,11 +479,11 @@ inline bool rows_of_16(const LayerArgs& a) {
 
 // One workgroup per tile; more threads than a launch holds are refused by the
 // argument checks.
-template <class T, class K>
+template <class T, int KS = 1, class K>
 hipError_t launch_tiles(K kernel, const LayerArgs& a, hipStream_t s) {
     const long long tm = ((long long)a.M + T::BM - 1) / T::BM, tn = ((long long)a.N + T::COLS - 1) / T::COLS;
-    if (tm * tn * T::OUTS * T::NT > 0xFFFFFFFFll) return hipErrorInvalidValue;
-    kernel<<<(unsigned)(tm * tn * T::OUTS), T::NT, 0, s>>>(a, (int)tm, (int)tn);
+    if (tm * tn * T::OUTS * KS * T::NT > 0xFFFFFFFFll) return hipErrorInvalidValue;
+    kernel<<<(unsigned)(tm * tn * T::OUTS), KS * T::NT, 0, s>>>(a, (int)tm, (int)tn);
     return hipGetLastError();
 }
 
