@@ -24,17 +24,21 @@
 // of the banks, and their line_at differ.)  Rows across k lie as in layer_tile.h,
 // 64 of them, lane half g's from 32 g on.
 //
-// K that is no whole number of stages: the first stage begins below k = 0, where
-// its lanes copy zeros.  The rows past M (N) of the last tiles are the last row
-// again, the columns past the matrix the tile's first ones: what they give is
-// not stored.
+// K that is no whole number of stages: what is left of it is the first stage, the
+// others follow from k = 0 on.  Lanes of that stage past K copy zeros, and where K
+// ends within 16 bytes of rows along k, the elements behind it (of the pitch, or
+// of the 16 bytes that the matrix's last row ends in) are cleared in LDS before
+// they are read.  (That stage alone is laid and read outside the loop.)  The rows
+// past M (N) of the last tiles are the last row again, the columns past the matrix
+// the tile's first ones: what they give is not stored.
 #pragma once
 
 #include "layer_tile.h"
 
 namespace sgemm {
-// Whether the kernel below takes a product: rows of whole 16 bytes, lane offsets
-// of 32 bits, and for the sum of two products whole stages and one pitch for both.
+// Whether the kernel below takes a product: rows that begin on 16 bytes, lane
+// offsets of 32 bits, and for the sum of two products whole stages and one pitch
+// for both.
 template <class T>
 inline bool big_fits(const LayerArgs& a) {
     const int nb = T::GATED || T::PAIRS == 2 ? 2 : 1, na = T::OUTS == 2 || T::PAIRS == 2 ? 2 : 1;
@@ -42,9 +46,8 @@ inline bool big_fits(const LayerArgs& a) {
         if (!mx_aligned(a.A[i], a.lda[i], 16) || !mx_dma_reach(a.lda[i], 512)) return false;
     for (int i = 0; i < nb; ++i)
         if (!mx_aligned(a.B[i], a.ldb[i], 16) || !mx_dma_reach(a.ldb[i], 512)) return false;
-    if (!T::A_ACROSS && (long long)a.K * T::ES % 16 != 0) return false;
     if (T::PAIRS == 2 && (a.K % (2 * T::KST) != 0 || a.lda[0] != a.lda[1] || a.ldb[0] != a.ldb[1])) return false;
-    return a.K >= 2 * T::KST;   // a stage at least: the first one alone may begin below k = 0
+    return a.K >= 2 * T::KST;   // a stage at least: the last one requested has to be whole
 }
 
 #ifdef __HIPCC__
@@ -67,6 +70,21 @@ __device__ __forceinline__ void mfma_in(floatx16& acc, u32x4 a, u32x4 b) {
 }
 
 __device__ __forceinline__ int line_at(int r) { return r >> 1 & 7; }
+
+// Which stage of a matrix is taken as number s: what is left of K first (the sum
+// of two products has whole stages only).
+template <int PAIRS>
+__device__ __forceinline__ int stage_k(int s, int each, bool far) {
+    if constexpr (PAIRS == 2) return far ? s - each : s;
+    return s == 0 ? each - 1 : s - 1;
+}
+// Zeros behind the first n bytes of row r of a stage, up to the next 16.
+__device__ __forceinline__ void clear_behind(unsigned char* stage, int r, int n) {
+    unsigned* const w = reinterpret_cast<unsigned*>(stage + r * 128 + 16 * ((n >> 4) ^ line_at(r)));
+    const int last = n >> 2 & 3;   // the word that n ends in
+    w[last] = n & 3 ? w[last] & ((1u << 8 * (n & 3)) - 1u) : 0u;
+    for (int i = last + 1; i < 4; ++i) w[i] = 0u;
+}
 
 constexpr int kUnits = 5;
 
@@ -109,9 +127,9 @@ void big_kernel(LayerArgs p, int tiles_m, int tiles_n) {
     const int nlast = (int)min((long long)p.N - 1 - n0, (long long)T::COLS - 1);
     const unsigned lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
 
-    // Stages: `each` of a pair of matrices, the first `pad` k below zero.
+    // Stages: `each` of a pair of matrices, the first with `left` of k.
     const int each = (int)(((long long)p.K + KST - 1) / KST), nst = each * T::PAIRS;
-    const int pad = (int)((long long)each * KST - p.K);
+    const int left = (int)(p.K - (each - 1ll) * KST);
 
     // DMA: instruction v of a unit fills its bytes 1024 v + 16 lane.  Along k: row
     // 8 v + lane / 8, place lane % 8.  Across: W / 8 places to a k row.  Lane
@@ -154,12 +172,12 @@ void big_kernel(LayerArgs p, int tiles_m, int tiles_n) {
     const long long a_pair = T::PAIRS == 2 ? p.A[1] - p.A[0] : 0, b_pair = T::PAIRS == 2 ? p.B[1] - p.B[0] : 0;
     auto a_step = [&](int s) __attribute__((always_inline)) {
         const bool far = T::PAIRS == 2 && s >= each;
-        const long long k = (long long)(far ? s - each : s) * KST - pad;
+        const long long k = stage_k<T::PAIRS>(s, each, far) * (long long)KST;
         return (T::A_ACROSS ? k * p.lda[pa] : k * ES) + (far ? a_pair : 0);
     };
     auto b_step = [&](int s) __attribute__((always_inline)) {
         const bool far = T::PAIRS == 2 && s >= each;
-        const long long k = (long long)(far ? s - each : s) * KST - pad;
+        const long long k = stage_k<T::PAIRS>(s, each, far) * (long long)KST;
         return (T::B_ACROSS ? k * p.ldb[0] : k * ES) + (far ? b_pair : 0);
     };
     auto to_of = [&](int unit, int u) __attribute__((always_inline)) {
@@ -287,20 +305,28 @@ void big_kernel(LayerArgs p, int tiles_m, int tiles_n) {
         });
     };
 
-    // The first stage, its lanes below k = 0 from zeros, and A of the second.
+    // The first stage, its lanes past K from zeros, and A of the second.
     {
         const unsigned char* const zero = reinterpret_cast<const unsigned char*>(&kZero16);
         const long long sa = a_step(0), sb = b_step(0), next = a_step(min(1, nst - 1));
 #pragma unroll
         for (int u = 0; u < NQ; ++u)
-            lds_dma16(akk[u] >= pad ? abase + sa + aoff[u] : zero, __builtin_amdgcn_readfirstlane(to_of(0, u)));
+            lds_dma16(akk[u] < left ? abase + sa + aoff[u] : zero, __builtin_amdgcn_readfirstlane(to_of(0, u)));
 #pragma unroll
         for (int u = 0; u < NQ; ++u)
-            lds_dma16(bkk[u] >= pad ? bbase[second(u)] + sb + boff[u] : zero, __builtin_amdgcn_readfirstlane(to_of(1, u)));
+            lds_dma16(bkk[u] < left ? bbase[second(u)] + sb + boff[u] : zero, __builtin_amdgcn_readfirstlane(to_of(1, u)));
 #pragma unroll
         for (int u = 0; u < NQ; ++u) request_a(u, 2, next);
     }
     barrier(NQ);
+    if constexpr (!T::A_ACROSS && !T::B_ACROSS)
+        if (left * ES % 16 != 0) {
+            if ((int)threadIdx.x < W) {
+                clear_behind(lds, threadIdx.x, left * ES);
+                clear_behind(lds + UNIT, threadIdx.x, left * ES);
+            }
+            barrier(NQ);
+        }
     static_for<NRD>([&](auto r) { read_op(first, first, r); });
     int s = 0;
     for (;;) {

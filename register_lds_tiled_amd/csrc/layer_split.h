@@ -34,6 +34,7 @@ __global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int til
     constexpr int A_BYTES = 2 * T::SA, B_BYTES = 2 * T::SB, STAGE = A_BYTES + B_BYTES, MINE = RING * STAGE;
     constexpr int AQ = A_BYTES / 1024, BQ = B_BYTES / 1024, NDMA = AQ + BQ;
     constexpr int PART = BM * T::STR * 4;
+    static_assert(BM <= 64 && BN <= 64, "a lane to each row");
     static_assert(T::NW == 1 && PART <= MINE, "a wave's part of the result in its ring");
     __shared__ __attribute__((aligned(1024))) unsigned char lds[kSplit * MINE];
     const int per = tiles_m * tiles_n;
@@ -48,9 +49,9 @@ __global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int til
     const int nlast = (int)min((long long)p.N - 1 - n0, (long long)T::COLS - 1);
     const unsigned ring = __builtin_amdgcn_readfirstlane(lds_addr(lds)) + (unsigned)(wave * MINE);
 
-    // Stages as in the large tiles' kernel: the first begins `pad` k below zero.
+    // Stages as in the large tiles' kernel: the first has what is left of K.
     const int each = (int)(((long long)p.K + KST - 1) / KST), nst = each * T::PAIRS;
-    const int pad = (int)((long long)each * KST - p.K);
+    const int left = (int)(p.K - (each - 1ll) * KST);
     const int mine = (nst - wave + kSplit - 1) / kSplit;   // this wave's
     auto along = [&](int v, int row, long long ld, int& kk) __attribute__((always_inline)) {
         const int c = (lane & 7) ^ line_at(8 * v + (lane >> 3));
@@ -90,18 +91,18 @@ __global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int til
     auto request = [&](int i) __attribute__((always_inline)) {
         const int s = i * kSplit + wave;
         const int pair = T::PAIRS == 2 && s >= each ? 1 : 0;
-        const long long k = (long long)(s - pair * each) * KST - pad;
+        const long long k = stage_k<T::PAIRS>(s, each, pair) * (long long)KST;
         const unsigned char* const a = abase + (T::A_ACROSS ? k * p.lda[pa] : k * ES) + (pair ? p.A[1] - p.A[0] : 0);
         const long long b = (T::B_ACROSS ? k * p.ldb[0] : k * ES) + (pair ? p.B[1] - p.B[0] : 0);
         const unsigned to = ring + (unsigned)(i % RING * STAGE);
-        if (s == 0 && pad > 0) {   // lanes below k = 0 copy zeros
+        if (s == 0 && left < KST) {   // lanes past K copy zeros
             const unsigned char* const zero = reinterpret_cast<const unsigned char*>(&kZero16);
 #pragma unroll
             for (int u = 0; u < AQ; ++u)
-                lds_dma16(akk[u] >= pad ? a + aoff[u] : zero, __builtin_amdgcn_readfirstlane(to + 1024u * u));
+                lds_dma16(akk[u] < left ? a + aoff[u] : zero, __builtin_amdgcn_readfirstlane(to + 1024u * u));
 #pragma unroll
             for (int u = 0; u < BQ; ++u)
-                lds_dma16(bkk[u] >= pad ? bbase[u] + b + boff[u] : zero,
+                lds_dma16(bkk[u] < left ? bbase[u] + b + boff[u] : zero,
                           __builtin_amdgcn_readfirstlane(to + A_BYTES + 1024u * u));
         } else {
 #pragma unroll
@@ -148,6 +149,13 @@ __global__ __launch_bounds__(64 * kSplit) void split_kernel(LayerArgs p, int til
 #pragma unroll
     for (int i = 0; i < RING; ++i)
         if (i < mine) request(i);
+    if constexpr (!T::A_ACROSS && !T::B_ACROSS)
+        if (wave == 0 && left * ES % 16 != 0) {   // K ends within 16 bytes
+            wait_loads<0>();
+            if (lane < BM) clear_behind(lds, lane, left * ES);
+            if (lane < BN) clear_behind(lds + A_BYTES, lane, left * ES);
+            lane_order();
+        }
     int i = 0;
     for (; i + RING < mine; ++i) {
         wait_loads<(RING - 1) * NDMA>();
@@ -212,7 +220,10 @@ hipError_t launch_split(const LayerArgs& a, hipStream_t s) {
 // A product's tiles.  32 x 64 or 64 x 64 with divided k where they fit one round of
 // workgroups, one to a CU, the latter also two rounds of them (but for a single
 // row of tiles, which memory bounds: gated bf16 64 x 16384 x 4096 88 us, 65 in 128 x
-// 128); else 128 x 128 up to two to a CU, and 256 x 256 beyond.  us, K = 4096 (the
+// 128); else 128 x 128 up to two to a CU or up to eight stages, where filling and
+// draining a tile takes longer than its products (us, 128 x 128 and 256 x 256: int8
+// 2096 x 12416 x 1024 40 and 47, x 2048 73 and 69; gated bf16 2096 x 12416 x 128 39
+// and 48, x 512 73 and 77, x 1024 125 and 120), and 256 x 256 beyond.  us, K = 4096 (the
 // next larger choice in brackets): int8 64 x 4096 7.5 (9.6), 128 x 4096 9.6 (22),
 // 512 x 4096 19 (22), 1024 x 4096 23 (49); gated bf16 64 x 4096 19 (24), 128 x 4096 23
 // (54), 512 x 2048 35 (51), 1024 x 4096 73 (92), 1024 x 8192 147 and 111; dX 512 x 4096
@@ -249,7 +260,8 @@ hipError_t launch_form(const LayerArgs& a, hipStream_t s) {
     using S64 = Tile<F, E, OUT, 64, 64, 64, 64>;
     if (tiles(S32{}) <= a.cus) return launch_split<S32, 2>(a, s);
     if (tiles(S64{}) <= (a.M > 64 ? 2ll : 1ll) * a.cus) return launch_split<S64, 2>(a, s);
-    if (tiles(Mid{}) <= 2ll * a.cus) return launch_tiles<Mid>(big_kernel<Mid>, a, s);
+    if (tiles(Mid{}) <= 2ll * a.cus || Wide::PAIRS * (long long)a.K <= 8 * 2 * Wide::KST)
+        return launch_tiles<Mid>(big_kernel<Mid>, a, s);
     return launch_tiles<Wide>(big_kernel<Wide>, a, s);
 }
 

@@ -222,3 +222,45 @@ def test_large_products_repeat_and_replay():
             assert torch.equal(t, w)
         call()
         torch.cuda.synchronize()
+
+
+# k that ends within 16 bytes of rows that begin on them: the rest of the 16 holds
+# NaN (-128 in 8 bits), also behind the last row
+CUT = [65, 71, 127, 129, 135, 190, 263, 327, 513, 1001, 1990]
+
+
+@pytest.mark.parametrize("M,N", SIZES)
+def test_i8_rows_that_end_within_16_bytes(M, N):
+    gen = torch.Generator(device=DEV).manual_seed(M + 1)
+    for K in (CUT[2:] if M * N < 1 << 22 else CUT[3::3]):
+        A = torch.randint(-128, 128, (M, K), generator=gen, device=DEV)
+        B = torch.randint(-128, 128, (N, K), generator=gen, device=DEV)
+        want = A.double() @ B.double().t()
+        a, w, one = filled(A, torch.int8), filled(B, torch.int8), torch.ones(max(M, N), device=DEV)
+        C = room(M, N, torch.float32)
+        b.gemm_i8_f32(M, N, K, a, a.stride(0), one, w, w.stride(0), one, C, C.stride(0))
+        exact = want.abs() < 2 ** 24
+        assert bool((C.double() == want)[exact].all()), (M, N, K)
+        check(C, want, want.abs() * 2.0 ** -24, "f32", f"{M}x{N}x{K}")
+        assert untouched(C, N)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("M,N", SIZES)
+def test_gated_rows_that_end_within_16_bytes(M, N, t):
+    gen = torch.Generator(device=DEV).manual_seed(N + 1)
+    N //= 2
+    for K in (CUT if M * N < 1 << 21 else CUT[::3]):
+        X, G, U = (filled(s * torch.randn((r, K), generator=gen, device=DEV), TYPES[t])
+                   for r, s in ((M, 1.0), (N, K ** -0.5), (N, K ** -0.5)))
+        H, g, u = (room(M, N, TYPES[t]) for _ in range(3))
+        fn("gemm_gated", t)(M, N, K, *[v for m in (X, G, U, g, u, H) for v in (m, m.stride(0))], "none")
+        x, wg, wu = X.double(), G.double(), U.double()
+        rg, ru = x @ wg.t(), x @ wu.t()
+        T = (-(-K // 16) + 32) * 2.0 ** -23
+        eg, eu = T * (x.abs() @ wg.abs().t()), T * (x.abs() @ wu.abs().t())
+        what = f"{M}x{N}x{K} {t}"
+        check(g, rg, eg, t, what + " G")
+        check(u, ru, eu, t, what + " U")
+        check(H, rg * ru, eg * ru.abs() + rg.abs() * eu + eg * eu + 2.0 ** -24 * (rg * ru).abs(), t, what + " H")
+        assert untouched(H, N) and untouched(g, N) and untouched(u, N)
