@@ -423,6 +423,8 @@ SGEMM_API int gemm_i8_gated_f16(int M, int N, int K, const void *A, int lda, con
  * stored), all matrices of one 16-bit type, leading dimensions in elements.
  * Sums, act and the product are fp32; H is rounded once.  G and U, both or
  * neither NULL, receive g and u rounded to 16 bits, for the backward pass.
+ * For g = -infinity act is what its formula gives in fp32: NaN of SILU and both
+ * forms of GELU, as of -infinity times 0.
  * K == 0 stores zeros.
  */
 SGEMM_API int gemm_gated_bf16(int M, int N, int K, const void *X, int ldx,
