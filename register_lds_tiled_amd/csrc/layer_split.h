@@ -235,7 +235,11 @@ hipError_t launch_split(const LayerArgs& a, hipStream_t s) {
 // tiles have two groups of waves for alternate stages where there are 12 and no
 // more than two workgroups to a CU (us, one group and two: dX 1000 x 777 x 1500 35
 // and 25.5, 70 x 4095 x 4093 91 and 72, of 544 tiles 70.5 and 75; dW 70 x 4095 x
-// 4093 46 and 34, of 768 tiles 20 and 22).  Rows along k gain a tenth at most so.
+// 4093 46 and 34, of 768 tiles 20 and 22).  Half as large, with two groups (dX:
+// four), where those fit one to a CU and there are stages for them: fewer bytes to
+// a CU (us, without and with: int8 70 x 4095 x 4093 20 and 15.6, gated bf16 59 and
+// 40, 100 x 1001 x 1003 15.7 and 11.8, 300 x 500 x 333 8.5 and 7.2; dX 172 x 2207 x
+// 3981 65 and 57, 399 x 82 x 5485 76 and 57; dW of 200 and more gains nothing).
 template <Form F, Elem E, Elem OUT>
 hipError_t launch_form(const LayerArgs& a, hipStream_t s) {
     using Wide = Tile<F, E, OUT, 256, 256, 128, 128, 4>;
@@ -248,6 +252,12 @@ hipError_t launch_form(const LayerArgs& a, hipStream_t s) {
     if (!big_fits<Mid>(a)) {
         using Small = Tile<F, E, OUT, 64, G ? 128 : 64, 32, G ? 64 : 32>;
         if (!rows_of_16<Mid>(a)) return launch_tiles<Small>(tile_kernel<Small, true>, a, s);
+        if constexpr (F != Form::both) {
+            using Half = Tile<F, E, OUT, G ? 64 : 32, 64, 32, G ? 64 : 32>;
+            constexpr int KS = Half::PAIRS == 2 ? 4 : 2;
+            if (tiles(Half{}) <= a.cus && Half::PAIRS * (long long)a.K >= (Half::PAIRS == 2 ? 12 : 4) * 2 * Half::KST)
+                return launch_tiles<Half, KS>(tile_kernel<Half, false, KS>, a, s);
+        }
         if (3 * tiles(Mid{}) <= 2ll * a.cus) {
             if constexpr (Small::B_ACROSS)
                 if (tiles(Small{}) <= 2ll * a.cus && Small::PAIRS * (long long)a.K >= 12 * 2 * Small::KST)
