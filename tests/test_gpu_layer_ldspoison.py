@@ -82,3 +82,21 @@ def test_gradients(libs, M, N, K, odd):
         DG, DU = (x.contiguous() if not odd else x for x in (DG, DU))
         both(libs, f"gemm_gated_backward_{t}", (M, N, K), (X, WG, WU, G, U, DH, DG, DU, DX, DWG, DWU),
              (DG, DU, DX, DWG, DWU), (2,))
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 300, 135), (300, 1500, 1001), (1500, 2100, 327), (4200, 4300, 1101)])
+def test_rows_that_end_within_16_bytes(libs, M, N, K):
+    """What is behind K in the last 16 bytes is cleared between a stage's landing and
+    its first read."""
+    gen = torch.Generator(device=DEV).manual_seed(M + K)
+    codes = lambda s: torch.randint(-127, 128, s, generator=gen, dtype=torch.int8, device=DEV)  # noqa: E731
+    A, G, U = (padded(r, K, -K % 16, codes) for r in (M, N, N // 2))
+    s = torch.rand(max(M, N), generator=gen, device=DEV) * 0.01
+    C = torch.empty((M, N), device=DEV)
+    both(libs, "gemm_i8_f32", (M, N, K), (A, s, G, s, C), (C,))
+    H = torch.empty((M, N // 2), dtype=torch.bfloat16, device=DEV)
+    both(libs, "gemm_i8_gated_bf16", (M, N // 2, K), (A, s, G, s, U, s, H), (H,), (2,))
+    real = lambda s: 0.1 * torch.randn(s, generator=gen, device=DEV).half()  # noqa: E731
+    X, WG, WU = (padded(r, K, -K % 8, real) for r in (M, N // 2, N // 2))
+    g, u, h = (torch.empty((M, N // 2), dtype=torch.float16, device=DEV) for _ in range(3))
+    both(libs, "gemm_gated_f16", (M, N // 2, K), (X, WG, WU, g, u, h), (g, u, h), (3,))
