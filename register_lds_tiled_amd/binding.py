@@ -304,17 +304,19 @@ _tensor = ()
 _raw_stream = None
 _current_device = None
 _functions = {}
+_i8 = _f32 = None
 
 
 def _mx_setup():
     """torch, and its calls for the current device and its stream's handle."""
-    global _torch, _tensor, _raw_stream, _current_device
+    global _torch, _tensor, _raw_stream, _current_device, _i8, _f32
     import torch
     _mx_kinds()
     _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
                    or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _tensor = torch.Tensor
+    _i8, _f32 = torch.int8, torch.float32
     _torch = torch
 
 
@@ -456,7 +458,18 @@ def _act(act):
     return GATED_ACTS[act] if isinstance(act, str) else int(act)
 
 
+# A small call costs the host more than the GPU: the ordinary one (tensors on the
+# current device, the current stream) is checked in one expression, 0.4 to 0.7 us less than
+# the loop of _mx_call (2 us), which takes every other call and says what is wrong.
+
 def _i8_quantize(name, t, R, C, X, ldx, Q, ldq, S, stream, check):
+    if (type(X) is type(Q) is type(S) is _tensor and stream is None
+            and X.dtype in _MX_KINDS[t] and Q.dtype is _i8 and S.dtype is _f32
+            and 0 <= (dev := X.get_device()) == Q.get_device() == S.get_device() == _current_device()
+            and S.numel() >= R and S.is_contiguous()
+            and not (R | C | ldx | ldq) >> 31 and (fn := _functions.get(name))):
+        st = fn(R, C, X.data_ptr(), ldx, Q.data_ptr(), ldq, S.data_ptr(), _raw_stream(dev))
+        return _check(st) if check and st else st
     return _mx_call(name, (R, C), ((t, X, ldx), ("i8", Q, ldq), ("vector", S, R)), stream, check)
 
 
@@ -477,6 +490,13 @@ def gemm_i8_quantize_f16(R, C, X, ldx, Q, ldq, S, stream=None, *, check=True) ->
 
 
 def _i8_dequantize(name, t, R, C, Q, ldq, S, Y, ldy, stream, check):
+    if (type(Q) is type(S) is type(Y) is _tensor and stream is None
+            and Q.dtype is _i8 and S.dtype is _f32 and Y.dtype in _MX_KINDS[t]
+            and 0 <= (dev := Q.get_device()) == S.get_device() == Y.get_device() == _current_device()
+            and S.numel() >= R and S.is_contiguous()
+            and not (R | C | ldq | ldy) >> 31 and (fn := _functions.get(name))):
+        st = fn(R, C, Q.data_ptr(), ldq, S.data_ptr(), Y.data_ptr(), ldy, _raw_stream(dev))
+        return _check(st) if check and st else st
     return _mx_call(name, (R, C), (("i8", Q, ldq), ("vector", S, R), (t, Y, ldy)), stream, check)
 
 
@@ -496,6 +516,15 @@ def gemm_i8_dequantize_f16(R, C, Q, ldq, S, Y, ldy, stream=None, *, check=True) 
 
 
 def _i8_product(name, t, M, N, K, A, lda, SA, B, ldb, SB, C, ldc, stream, check):
+    if (type(A) is type(SA) is type(B) is type(SB) is type(C) is _tensor and stream is None
+            and A.dtype is B.dtype is _i8 and SA.dtype is SB.dtype is _f32 and C.dtype in _MX_KINDS[t]
+            and 0 <= (dev := A.get_device()) == SA.get_device() == B.get_device() == SB.get_device()
+            == C.get_device() == _current_device()
+            and SA.numel() >= M and SA.is_contiguous() and SB.numel() >= N and SB.is_contiguous()
+            and not (M | N | K | lda | ldb | ldc) >> 31 and (fn := _functions.get(name))):
+        st = fn(M, N, K, A.data_ptr(), lda, SA.data_ptr(), B.data_ptr(), ldb, SB.data_ptr(),
+                C.data_ptr(), ldc, _raw_stream(dev))
+        return _check(st) if check and st else st
     return _mx_call(name, (M, N, K), (("i8", A, lda), ("vector", SA, M), ("i8", B, ldb),
                                       ("vector", SB, N), (t, C, ldc)), stream, check)
 
@@ -541,6 +570,16 @@ def gemm_i8_gated_f16(M, N, K, A, lda, SA, BG, ldbg, SBG, BU, ldbu, SBU, H, ldh,
 
 def _gated(name, t, M, N, K, X, ldx, WG, ldwg, WU, ldwu, G, ldg, U, ldu, H, ldh, act, stream,
            check):
+    if (type(X) is type(WG) is type(WU) is type(H) is _tensor and G is U is stream is None
+            and X.dtype is WG.dtype is WU.dtype is H.dtype and X.dtype in _MX_KINDS[t]
+            and (code := GATED_ACTS.get(act)) is not None
+            and 0 <= (dev := X.get_device()) == WG.get_device() == WU.get_device() == H.get_device()
+            == _current_device()
+            and not (M | N | K | ldx | ldwg | ldwu | ldg | ldu | ldh) >> 31
+            and (fn := _functions.get(name))):
+        st = fn(M, N, K, X.data_ptr(), ldx, WG.data_ptr(), ldwg, WU.data_ptr(), ldwu, None, ldg,
+                None, ldu, H.data_ptr(), ldh, code, _raw_stream(dev))
+        return _check(st) if check and st else st
     return _mx_call(name, (M, N, K),
                     ((t, X, ldx), (t, WG, ldwg), (t, WU, ldwu), (t, G, ldg), (t, U, ldu),
                      (t, H, ldh)), stream, check, (_act(act),))

@@ -668,3 +668,39 @@ def test_another_stream_is_the_current_one():
         b.gemm_gated_bf16(M, N, K, y, K, w, K, w, K, None, 0, None, 0, H, N)
     torch.cuda.synchronize()
     assert torch.equal(H, ref)
+
+
+def test_checks_hold_after_a_first_call():
+    """What the binding refuses it refuses also where the same entry point has run."""
+    M, N, K = 8, 24, 32
+    i8 = torch.randint(-9, 9, (N, K), dtype=torch.int8, device=DEV)
+    A, S = i8[:M], torch.ones(N, device=DEV)
+    X, H = torch.randn((N, K), device=DEV).bfloat16(), torch.zeros((M, N), device=DEV).bfloat16()
+    C, Q = torch.zeros((M, N), device=DEV), torch.zeros_like(i8)
+    mm = lambda A=A, SA=S, C=C, M=M, ldc=N: b.gemm_i8_f32(M, N, K, A, K, SA, i8, K, S, C, ldc)  # noqa: E731
+    cast = lambda X=X, Q=Q, S=S, R=N: b.gemm_i8_quantize_bf16(R, K, X, K, Q, K, S)  # noqa: E731
+    back = lambda Q=Q, S=S, Y=X, C=K: b.gemm_i8_dequantize_bf16(N, C, Q, K, S, Y, K)  # noqa: E731
+    gated = lambda X=X, H=H, act="silu", K=K: b.gemm_gated_bf16(  # noqa: E731
+        M, N, K, X, 32, X, 32, X, 32, None, 0, None, 0, H, N, act)
+    for call in (mm, cast, back, gated):
+        for _ in range(2):
+            assert call() == b.SGEMM_OK
+    for call, wrong in ((mm, dict(A=X)), (mm, dict(SA=X)), (mm, dict(C=H)), (cast, dict(X=C)), (cast, dict(Q=X)),
+                        (back, dict(S=H)), (back, dict(Y=C)), (gated, dict(X=X.half())), (gated, dict(H=C))):
+        with pytest.raises(TypeError):
+            call(**wrong)
+    for call, wrong in ((mm, dict(A=A.cpu())), (mm, dict(SA=S[:M - 1])), (mm, dict(SA=torch.ones(2 * N, device=DEV)[::2])),
+                        (cast, dict(S=S[:3])), (cast, dict(X=X.cpu())), (back, dict(S=S[::2])), (back, dict(Q=Q.cpu())),
+                        (gated, dict(H=H.cpu())), (mm, dict(M=1 << 32)), (cast, dict(R=1 << 31))):   # too few scales
+        with pytest.raises(ValueError):
+            call(**wrong)
+    for call, wrong in ((mm, dict(ldc=-1 << 40)), (mm, dict(ldc=1 << 31)), (back, dict(C=1 << 35)),
+                        (gated, dict(K=1 << 31)), (gated, dict(act=1 << 33))):
+        with pytest.raises(OverflowError):
+            call(**wrong)
+    for call, wrong in ((mm, dict(M=-1)), (mm, dict(ldc=N - 1)), (cast, dict(R=-5)), (gated, dict(act=5)), (gated, dict(K=33))):
+        with pytest.raises(b.SgemmError):
+            call(**wrong)
+    with pytest.raises(KeyError):
+        gated(act="tanh")
+    torch.cuda.synchronize()
