@@ -223,7 +223,10 @@ hipError_t launch_split(const LayerArgs& a, hipStream_t s) {
 // 128); else 128 x 128 up to two to a CU or up to eight stages, where filling and
 // draining a tile takes longer than its products (us, 128 x 128 and 256 x 256: int8
 // 2096 x 12416 x 1024 40 and 47, x 2048 73 and 69; gated bf16 2096 x 12416 x 128 39
-// and 48, x 512 73 and 77, x 1024 125 and 120), and 256 x 256 beyond.  us, K = 4096 (the
+// and 48, x 512 73 and 77, x 1024 125 and 120), and 256 x 256 beyond, but where a
+// second round of those would be a quarter full (1.06 rounds: int8 4352 x 4096 x 4096
+// 97 and 109, gated bf16 4352 x 2048 x 4096 167 and 178; 1.25: 99 and 113, 173 and
+// 184, dW 190 and 186; 1.5: 116 and 118, 203 and 193).  us, K = 4096 (the
 // next larger choice in brackets): int8 64 x 4096 7.5 (9.6), 128 x 4096 9.6 (22),
 // 512 x 4096 19 (22), 1024 x 4096 23 (49); gated bf16 64 x 4096 19 (24), 128 x 4096 23
 // (54), 512 x 2048 35 (51), 1024 x 4096 73 (92), 1024 x 8192 147 and 111; dX 512 x 4096
@@ -270,7 +273,9 @@ hipError_t launch_form(const LayerArgs& a, hipStream_t s) {
     using S64 = Tile<F, E, OUT, 64, 64, 64, 64>;
     if (tiles(S32{}) <= a.cus) return launch_split<S32, 2>(a, s);
     if (tiles(S64{}) <= (a.M > 64 ? 2ll : 1ll) * a.cus) return launch_split<S64, 2>(a, s);
-    if (tiles(Mid{}) <= 2ll * a.cus || Wide::PAIRS * (long long)a.K <= 8 * 2 * Wide::KST)
+    const long long wide = tiles(Wide{});
+    if (tiles(Mid{}) <= 2ll * a.cus || Wide::PAIRS * (long long)a.K <= 8 * 2 * Wide::KST ||
+        (wide > a.cus && 4 * wide <= 5ll * a.cus))
         return launch_tiles<Mid>(big_kernel<Mid>, a, s);
     return launch_tiles<Wide>(big_kernel<Wide>, a, s);
 }

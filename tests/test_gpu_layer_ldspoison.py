@@ -100,3 +100,11 @@ def test_rows_that_end_within_16_bytes(libs, M, N, K):
     X, WG, WU = (padded(r, K, -K % 8, real) for r in (M, N // 2, N // 2))
     g, u, h = (torch.empty((M, N // 2), dtype=torch.float16, device=DEV) for _ in range(3))
     both(libs, "gemm_gated_f16", (M, N // 2, K), (X, WG, WU, g, u, h), (g, u, h), (3,))
+
+
+def test_the_largest_tiles(libs):
+    """More than eight stages in more than a round and a quarter of 256 x 256 tiles."""
+    for K in (1101, 2064):
+        test_rows_that_end_within_16_bytes(libs, 5300, 4300, K)
+    test_gradients(libs, 4700, 640, 4900, 0)
+    test_gradients(libs, 600, 2600, 4900, 0)

@@ -264,3 +264,24 @@ def test_gated_rows_that_end_within_16_bytes(M, N, t):
         check(u, ru, eu, t, what + " U")
         check(H, rg * ru, eg * ru.abs() + rg.abs() * eu + eg * eu + 2.0 ** -24 * (rg * ru).abs(), t, what + " H")
         assert untouched(H, N) and untouched(g, N) and untouched(u, N)
+
+
+# more than eight stages in more than a round and a quarter of 256 x 256 tiles, of each form
+def test_i8_in_the_largest_tiles():
+    test_i8(5300, 4300, True)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+def test_gated_in_the_largest_tiles(t):
+    test_gated(5300, 4300, True, t)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("M,N,K", [(4700, 640, 4900), (600, 2600, 4900)])
+def test_backward_in_the_largest_tiles(M, N, K, t):
+    test_backward(M, N, K, True, t)
+
+
+def test_rows_that_end_within_16_bytes_in_the_largest_tiles():
+    test_i8_rows_that_end_within_16_bytes(5300, 4300)
+    test_gated_rows_that_end_within_16_bytes(5300, 4300, "bf16")

@@ -165,7 +165,7 @@ def test_every_kernel_is_launched_by_some_call(lib):
                             call(backward(lib, t, M, N, K, pad, dx, dw))
     for t in ("bf16", "f16"):
         call(backward(lib, t, 4200, 64, 4096, 0, True, False))
-        call(backward(lib, t, 4200, 1024, 4096, 0, True, False))
+        call(backward(lib, t, 4200, 1024, 8192, 0, True, False))
         call(i8_gated(lib, t, 4200, 4096, 2048, 0))
     for t in ("f32", "bf16", "f16"):
         call(i8(lib, t, 4200, 8192, 2048, 0))
