@@ -115,9 +115,12 @@ __device__ __forceinline__ float act_of(float x) {
     }
     return x;
 }
-// Activation and slope.
+// Activation and slope of a gate sum as it was kept, in 16 bits: -infinity stands
+// for a finite sum as well, so the activation's factor is held at a number whose
+// product has long been the limit, 0 (NaN stays: the other factor is NaN then).
 template <int ACT>
 __device__ __forceinline__ void act_and_slope(float x, float& a, float& d) {
+    const float low = fmaxf(x, -1e4f);
     if constexpr (ACT == 0) {
         a = x;
         d = 1.f;
@@ -126,15 +129,15 @@ __device__ __forceinline__ void act_and_slope(float x, float& a, float& d) {
         d = x <= 0.f ? 0.f : 1.f;
     } else if constexpr (ACT == 2) {
         const float s = sigmoid(x), h = held(x, 100.f);
-        a = x * s;
+        a = low * s;
         d = s * (1.f + h * (1.f - s));
     } else if constexpr (ACT == 3) {
         const float p = 0.5f * erfcf(x * -0.70710678118654752f), h = held(x, 30.f);
-        a = x * p;
+        a = low * p;
         d = p + h * (0.5f * kGeluC) * exp_of(-0.5f * h * h);
     } else {
         const float h = held(x, 30.f), s = sigmoid(2.f * kGeluC * (h + 0.044715f * h * h * h));
-        a = x * s;
+        a = low * s;
         d = s + 2.f * kGeluC * h * s * (1.f - s) * (1.f + 0.134145f * h * h);
     }
 }
