@@ -441,9 +441,10 @@ SGEMM_API int gemm_gated_f16(int M, int N, int K, const void *X, int ldx,
  *     DWG = DG^T.X               DWU = DU^T.X                    (N x K)
  * all of one 16-bit type, sums and act in fp32.  Each result is rounded once;
  * DX, DWG and DWU are products of DG and DU as rounded.  ReLU's slope at 0 is 0.
- * G holds -infinity for a sum below its type's range, of which the forward pass
- * took the finite value: act and act' are their limits there, 0 of SILU and both
- * forms of GELU.
+ * G and U hold infinities for sums beyond their type's range, of which the forward
+ * pass took the finite values: at G = -infinity act and act' are their limits, 0 of
+ * SILU and both forms of GELU, and where act' is 0 so is DG, also for an infinite
+ * U.  Otherwise infinities and NaN are multiplied as they are.
  * - DX may be NULL, then it is not computed, and WG, WU and the three leading
  *   dimensions are not looked at; DWG and DWU may both be NULL, then they are
  *   not computed and neither they nor X are looked at (one of the two ->

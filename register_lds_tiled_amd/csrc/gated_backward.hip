@@ -7,7 +7,9 @@ namespace sgemm {
 namespace {
 
 // A thread takes eight columns down the rows: three reads, two writes, bound by
-// memory.
+// memory.  An infinity in U stands for a finite sum beyond its type's range as
+// well (act_and_slope has G's): where the slope is 0, so is dG.  (The branch for
+// them: 4096 x 8192 bf16 SiLU 62.8 us, 62.1 without.)
 template <Elem E>
 __global__ __launch_bounds__(256) void gated_slopes_kernel(GateArgs p, int shift) {
     const int units = (int)(((long long)p.N + 7) / 8);
@@ -17,17 +19,23 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(GateArgs p, int shift
     const long long rows = (long long)gridDim.y << (8 - shift);
     with_act(p.act, [&](auto act) __attribute__((always_inline)) {
         for (long long r = ((long long)blockIdx.y << (8 - shift)) + (threadIdx.x >> shift); r < p.M; r += rows) {
-            float g[8], u[8], dh[8], dg[8], du[8];
+            float g[8], u[8], dh[8], dg[8], du[8], d[8], top = 0.f;
             load8<E>(p.G + 2 * r * p.ldg, 8 * i, p.N, g);
             load8<E>(p.U + 2 * r * p.ldu, 8 * i, p.N, u);
             load8<E>(p.DH + 2 * r * p.lddh, 8 * i, p.N, dh);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float a, d;
-                act_and_slope<act>(g[e], a, d);
-                dg[e] = dh[e] * u[e] * d;
+                float a;
+                act_and_slope<act>(g[e], a, d[e]);
                 du[e] = dh[e] * a;
+                top = fmaxf(top, __builtin_fabsf(u[e]));
             }
+            if (top == __builtin_inff()) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = d[e] == 0.f && __builtin_isinf(u[e]) ? 0.f : u[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dg[e] = dh[e] * u[e] * d[e];
             typedef type_of<E> O;
             store8<E>(reinterpret_cast<O*>(p.DG) + r * p.lddg + 8 * i, dg, n);
             store8<E>(reinterpret_cast<O*>(p.DU) + r * p.lddu + 8 * i, du, n);

@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 
 from oracle import layer as o
+from register_lds_tiled_amd import binding as b
 from tests.test_gpu_layer import Mat, act_error, backward, fn, near, product_error
 
 torch = pytest.importorskip("torch")
@@ -130,3 +131,50 @@ def test_a_gate_that_is_no_number_stays_so(act, t):
     assert where(du) == {(1, 3), (9, 20), (13, 41)}      # infinity times the limit 0 is none
     assert where(dg) == {(1, 3), (5, 8), (9, 20), (13, 41)}
     assert du[12, 40] == 0 and dg[12, 40] == 0
+
+
+@pytest.mark.parametrize("act", ("relu", *CURVED))
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_infinite_u_behind_a_shut_gate(act, t):
+    """U of either infinity: no gradient where the slope is 0, infinite ones where it is
+    not; dU does not look at U."""
+    M, N, K = 130, 72, 64
+    rng = np.random.default_rng(7)
+    X, WG, WU = (Mat(rng.standard_normal(s), t) for s in ((M, K), (N, K), (N, K)))
+    G, U, DH = (rng.standard_normal((M, N)) for _ in range(3))
+    shut = -1.0 if act == "relu" else -1000.0
+    for i, (g, u) in enumerate(((shut, np.inf), (shut, -np.inf), (-np.inf, np.inf), (-np.inf, -np.inf))):
+        G[20 + i, 3 + 9 * i], U[20 + i, 3 + 9 * i] = g, u
+    if act == "relu":
+        G[30, 5], U[30, 5] = 0.0, np.inf
+    G, U, DH = (Mat(v, t) for v in (G, U, DH))
+    got = [m.get().double().numpy() for m in backward(t, M, N, K, X, WG, WU, G, U, DH, act)]
+    assert all(np.isfinite(x).all() for x in got)
+    assert (got[0][np.isinf(U.value)] == 0).all()
+    U.value[50, 60] = np.inf                       # an open gate
+    U2, G.value[50, 60] = U.value, 2.0
+    got = [m.get().double().numpy() for m in backward(t, M, N, K, X, WG, WU, Mat(G.value, t), Mat(U2, t), DH, act)]
+    assert {tuple(map(int, i)) for i in np.argwhere(~np.isfinite(got[0]))} == {(50, 60)} and np.isinf(got[0][50, 60])
+    assert np.isfinite(got[1]).all()
+
+
+def test_infinite_u_of_a_sum_that_fp32_holds():
+    """Forward and backward: a channel whose second projection passes binary16's range
+    behind a gate that ReLU shuts."""
+    M, N, K, t = 33, 40, 64, "f16"
+    rng = np.random.default_rng(9)
+    X, WG, WU = rng.standard_normal((M, K)), rng.standard_normal((N, K)) / 8, rng.standard_normal((N, K)) / 8
+    X[:, :3] = 0
+    X[6, :3] = 1
+    WG[:, :3], WU[:, :3] = 0, 0
+    WG[11, 2], WU[11, :2] = -40.0, (60000.0, 30000.0)
+    X, WG, WU = (Mat(v, t) for v in (X, WG, WU))
+    DH = rng.standard_normal((M, N))
+    DH[:6, 11], DH[7:, 11] = 0, 0
+    DH = Mat(DH, t)
+    H, G, U = (Mat(None, t, 0, 0, M, N) for _ in range(3))
+    b.gemm_gated_f16(M, N, K, *X.at, *WG.at, *WU.at, *G.at, *U.at, *H.at, "relu")
+    G.value, U.value = G.get().double().numpy(), U.get().double().numpy()
+    assert np.isfinite(H.get().numpy()).all() and U.value[6, 11] == np.inf and G.value[6, 11] < 0
+    got = backward(t, M, N, K, X, WG, WU, G, U, DH, "relu")
+    assert all(np.isfinite(m.get().numpy()).all() for m in got)
