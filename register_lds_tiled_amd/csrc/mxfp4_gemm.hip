@@ -97,7 +97,7 @@ __global__ __launch_bounds__(Cfg::NT) void mx_tile_kernel(MxGemmArgs p, int tile
     const int wm = (wave / Cfg::WAVES_N) * Cfg::WM, wn = (wave % Cfg::WAVES_N) * Cfg::WN;
     const int li = lane & 31, g = lane >> 5;
     const long long m0 = (long long)tm * BM, n0 = (long long)tn * BN;
-    const long long ks = ((long long)p.K + 31) / 32;
+    const long long ks = ((long long)p.K + 31) / 32, len = ((long long)p.K + 1) / 2;
 
     // The thread's chunks and the row of its scales.  Rows past the matrix
     // read the last one: their products are not stored.
@@ -122,8 +122,10 @@ __global__ __launch_bounds__(Cfg::NT) void mx_tile_kernel(MxGemmArgs p, int tile
             __builtin_memcpy(s, ssrc + k0 / 32, 8);
         } else {
 #pragma unroll
-            for (int u = 0; u < CH; ++u)
-                v[u] = mx_codes16(src[u], k0 / 2 + 16 * ((tid + u * NT) & 7), p.K);
+            for (int u = 0; u < CH; ++u) {
+                const long long at = k0 / 2 + 16 * ((tid + u * NT) & 7);
+                v[u] = len >= 16 ? mx_load16(src[u], at, len) : mx_codes16(src[u], at, p.K);
+            }
             mx_scales<8>(ssrc, k0 / 32, ks, s);
         }
     };
@@ -131,6 +133,10 @@ __global__ __launch_bounds__(Cfg::NT) void mx_tile_kernel(MxGemmArgs p, int tile
     floatx16 acc[FM][FN] = {};
     fetch(0);
     for (long long k0 = 0; k0 < p.K; k0 += Cfg::BK) {
+        if (k0 + Cfg::BK > p.K && len >= 16) {
+#pragma unroll
+            for (int u = 0; u < CH; ++u) v[u] = mx_end_codes16(v[u], k0 / 2 + 16 * ((tid + u * NT) & 7), p.K);
+        }
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < CH; ++u) {

@@ -49,28 +49,43 @@ __global__ __launch_bounds__(Cfg::NT, 1) void mx_wtile_kernel(MxGemmArgs p, int 
     const int wm = (wave / Cfg::WAVES_N) * Cfg::WM, wn = (wave % Cfg::WAVES_N) * Cfg::WN;
     const int li = lane & 15, g = lane >> 4;
     const long long m0 = (long long)tm * BM, n0 = (long long)tn * BN;
-    const long long ka = 2ll * p.K, ks = ((long long)p.K + 31) / 32;
+    const long long ka = 2ll * p.K, kb = ((long long)p.K + 1) / 2, ks = ((long long)p.K + 31) / 32;
+    const bool rows16 = kb >= 16;
 
     uint4 va[CA], vb[CB];
     unsigned s[1];
     auto fetch = [&](long long k0) {
+        auto load = [&](auto a_chunk, auto b_chunk) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < CA; ++u) {
-            const int id = tid + u * NT, r = id >> 4, c = id & 15;
-            const long long at = 2 * k0 + 16 * c;
-            va[u] = mx_bytes16(p.A + min(m0 + r, (long long)p.M - 1) * p.lda, at, ka);
-        }
+            for (int u = 0; u < CA; ++u) {
+                const int id = tid + u * NT, r = id >> 4, c = id & 15;
+                va[u] = a_chunk(p.A + min(m0 + r, (long long)p.M - 1) * p.lda, 2 * k0 + 16 * c);
+            }
 #pragma unroll
-        for (int u = 0; u < CB; ++u) {
-            const int id = tid + u * NT, r = id >> 2, c = id & 3;
-            vb[u] = mx_codes16(p.B + min(n0 + r, (long long)p.N - 1) * p.ldb, k0 / 2 + 16 * c, p.K);
-        }
+            for (int u = 0; u < CB; ++u) {
+                const int id = tid + u * NT, r = id >> 2, c = id & 3;
+                vb[u] = b_chunk(p.B + min(n0 + r, (long long)p.N - 1) * p.ldb, k0 / 2 + 16 * c);
+            }
+        };
+        typedef const unsigned char* Row;
+        if (k0 + Cfg::BK > p.K && rows16)
+            load([&](Row row, long long at) { return mx_load16(row, at, ka); },
+                 [&](Row row, long long at) { return mx_load16(row, at, kb); });
+        else
+            load([&](Row row, long long at) { return mx_bytes16(row, at, ka); },
+                 [&](Row row, long long at) { return mx_codes16(row, at, p.K); });
         mx_scales<4>(p.SB + min(n0 + (tid < BN ? tid : 0), (long long)p.N - 1) * p.ldsb, k0 / 32, ks, s);
     };
 
     mx_f4 acc[FM][FN] = {};
     fetch(0);
     for (long long k0 = 0; k0 < p.K; k0 += Cfg::BK) {
+        if (k0 + Cfg::BK > p.K && rows16) {
+#pragma unroll
+            for (int u = 0; u < CA; ++u) va[u] = mx_end16(va[u], 2 * k0 + 16 * ((tid + u * NT) & 15), ka);
+#pragma unroll
+            for (int u = 0; u < CB; ++u) vb[u] = mx_end_codes16(vb[u], k0 / 2 + 16 * ((tid + u * NT) & 3), p.K);
+        }
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < CA; ++u) {
