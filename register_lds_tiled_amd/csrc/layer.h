@@ -93,9 +93,14 @@ constexpr int size_of = sizeof(type_of<T>);
 // y = sqrt(2/pi) (x + 0.044715 x^3); s(x) = 1 / (1 + exp(-x)).
 //
 // The exponential is 2^(x log2 e) by the hardware's 2^x, the quotient by its
-// reciprocal (an ulp each); the argument's rounding makes a relative error of at
-// most 2^-24 |x|, so these are good to 2^-17 where they are not negligible: the
-// results are rounded to 16 bits.
+// reciprocal, an ulp each.  What an argument's roundings make of it grows with the
+// argument, so an activation is off by at most 2^-23 (8 + 4 z) of its value, z = |x|
+// for SiLU, |2y| for the tanh form (its cubic has four roundings more) and x^2 for
+// GELU, whose erfc turns its argument's relative error into x^2 of it: 2^-18 up to
+// |x| = 2.  (With every rounding emulated the worst is 2^-18.0 for SiLU, 2^-15.8 for
+// the tanh form and 2^-16.4 for GELU, all where results are next to 2^-119.)
+// Results are rounded to 16 bits, half a step being 2^-8 and 2^-11 of them.  Below
+// 2^-119 they may be 0, where the reciprocal has no normal number.
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504089f); }
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + exp_of(-x)); }
 // Within +-lim, NaN as it is.  Past the limit a slope is constant, and the
