@@ -1,6 +1,12 @@
 // gated_backward.hip -- the gated block's gradients in 16 bits: dG and dU element
 // by element, dX = dG.Wg + dU.Wu as one product over both, dWg = dG^T.X and
 // dWu = dU^T.X in one launch.
+//
+// The products take dG and dU as the call returns them, rounded to 16 bits, because
+// the matrix instructions take 16-bit operands; with fp32 dG and dU each would be two
+// terms, at twice the instructions.  That rounding and the result's own are of one
+// size, so dX, dWg and dWu are off by sqrt 2 of what the latter alone gives (1.5
+// times where a few large channels of X carry a gradient).
 #include "layer_split.h"
 
 namespace sgemm {
