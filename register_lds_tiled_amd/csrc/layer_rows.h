@@ -196,9 +196,9 @@ hipError_t launch_few(const LayerArgs& a, hipStream_t s) {
 
 // Whether a product takes the kernel above: at most 32 rows, or 64 where rows do
 // not begin on 16 bytes or are shorter than a stage of the tiles (else tiles whose
-// waves divide k: 64 rows, 8192 x 8192 int8 18.7 us against 28, 4096 x 4096 out of the
-// last-level cache 7.5 against 12); columns that a launch of 512 threads per 16 holds; and rows in reach
-// of 32-bit offsets.
+// waves divide k: 64 rows, 8192 x 8192 int8 18.7 us against 28, 4096 x 4096 from the
+// last-level cache 7.5 against 12); columns that a launch of 512 threads per 16
+// holds; and rows in reach of 32-bit offsets.
 inline bool few_rows(const LayerArgs& a, int size, bool gated) {
     auto whole = [&](const void* p, long long ld) { return mx_aligned(p, ld, 16); };
     const bool aligned = whole(a.A[0], a.lda[0]) && whole(a.B[0], a.ldb[0]) && (!gated || whole(a.B[1], a.ldb[1])) &&

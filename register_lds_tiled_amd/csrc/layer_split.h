@@ -227,10 +227,10 @@ hipError_t launch_split(const LayerArgs& a, hipStream_t s) {
 // second round of those would be a quarter full (1.06 rounds: int8 4352 x 4096 x 4096
 // 97 and 109, gated bf16 4352 x 2048 x 4096 167 and 178; 1.25: 99 and 113, 173 and
 // 184, dW 190 and 186; 1.5: 116 and 118, 203 and 193).  us, K = 4096 (the
-// next larger choice in brackets; 8-bit operands out of the last-level cache): int8 64 x 4096 7.5 (9.6), 128 x 4096 9.6 (22),
-// 512 x 4096 19 (22), 1024 x 4096 23 (49); gated bf16 64 x 4096 19 (24), 128 x 4096 23
-// (54), 512 x 2048 35 (51), 1024 x 4096 73 (92), 1024 x 8192 147 and 111; dX 512 x 4096
-// 69 (100).
+// next larger choice in brackets; 8-bit operands from the last-level cache): int8 64
+// x 4096 7.5 (9.6), 128 x 4096 9.6 (22), 512 x 4096 19 (22), 1024 x 4096 23 (49);
+// gated bf16 64 x 4096 19 (24), 128 x 4096 23 (54), 512 x 2048 35 (51), 1024 x 4096 73
+// (92), 1024 x 8192 147 and 111; dX 512 x 4096 69 (100).
 // Rows off 16 bytes go through registers, in 64 x 64 (gated: x 128) products where
 // 128 x 128 would leave a third of the CUs idle (us, small and large: int8 1000 x
 // 1500 x 777 12.2 and 14.7, its dW 20 and 22, dX 26 and 34; the gated form of 192
