@@ -54,6 +54,7 @@ import glob
 import hashlib
 import json
 import os
+import re
 import sys
 import time
 
@@ -98,16 +99,30 @@ def hash_path(args) -> str:
     return "skinny" if args.workload in W.SKINNY else "f32"
 
 
+def abi_part(sources: str) -> str:
+    """What the ABI header says of what `sources` name: its macros and
+    declarations without comments, those of other families left out."""
+    with open(os.path.join(ROOT, "include", "sgemm.h"), encoding="utf-8") as fh:
+        text = re.sub(r"/\*.*?\*/", " ", fh.read(), flags=re.S)
+    used = set(re.findall(r"\w+", sources))
+    parts = re.findall(r"^#define\s+(\w+)(.*)$|^SGEMM_API\b([^;]*?(\w+)\s*\([^;]*);", text, re.M)
+    return "\n".join(" ".join(((macro + value) if macro else decl).split())
+                     for macro, value, decl, name in parts if (macro or name) in used)
+
+
 def source_hash(path: str = "f32") -> str:
-    """Hash of one path's HIP sources and the ABI header."""
+    """Hash of one path's HIP sources and of their part of the ABI header (a new
+    family's declarations, or a comment there, change no kernel of this one)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "register_lds_tiled_amd", "csrc")
-    files = [os.path.join(csrc, n) for n in PATH_SOURCES[path]]
-    files.append(os.path.join(ROOT, "include", "sgemm.h"))
-    for f in files:
-        h.update(os.path.basename(f).encode())
-        with open(f, "rb") as fh:
-            h.update(fh.read())
+    text = ""
+    for f in PATH_SOURCES[path]:
+        with open(os.path.join(csrc, f), "rb") as fh:
+            data = fh.read()
+        h.update(f.encode())
+        h.update(data)
+        text += data.decode("utf-8")
+    h.update(abi_part(text).encode())
     return h.hexdigest()[:16]
 
 
